@@ -1,6 +1,7 @@
-"""GB300 (sm_103a) FlashAttention forward -- thin Python binding of the C ABI.
+"""GB300 (sm_103a) FlashAttention -- thin Python binding of the C ABI.
 
-Every step of the forward pass runs in the CUDA library ``_build/libfa_gb300.so``
+Every step of the forward and backward passes and of the operators around the
+paged decode (shared prefixes, key weights, cache eviction) runs in the CUDA library ``_build/libfa_gb300.so``
 (see ``include/fa_gb300.h``).  This module only marshals torch tensors into
 ``fa_tensor_t`` descriptors, allocates outputs/workspace with torch on the
 current stream, and raises on any non-OK status.  There is no fallback: if the
@@ -8,6 +9,7 @@ library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -27,7 +29,9 @@ MOD_NONE, MOD_ALIBI, MOD_SOFTCAP = 0, 1, 2
 EXPORTED = ("fa_fwd_varlen", "fa_fwd_workspace_bytes", "fa_fwd_default_splits", "fa_combine",
             "fa_last_error", "fa_get_device_error", "fa_version", "fa_fwd_varlen_noalloc",
             "fa_fwd_plan_create", "fa_fwd_plan_launch", "fa_fwd_plan_destroy", "fa_bwd_varlen",
-            "fa_bwd_workspace_bytes")
+            "fa_bwd_workspace_bytes", "fa_fwd_shared_prefix", "fa_shared_prefix_plan_create",
+            "fa_shared_prefix_workspace_bytes", "fa_shared_prefix_default_splits", "fa_key_weights",
+            "fa_key_weights_plan_create", "fa_cache_evict")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -96,6 +100,11 @@ class Launch(ctypes.Structure):
                 ("flags", ctypes.c_int32)]
 
 
+class SharedPrefix(ctypes.Structure):
+    _fields_ = [("cu_groups", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("num_groups", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("num_splits", ctypes.c_int32)]
+
+
 # fa_launch_t.flags: P * V on e4m3 operands (opt-in precision mode, e4m3 q
 # with e4m3 caches; see FA_FLAG_PV_E4M3 in fa_gb300.h)
 FLAG_PV_E4M3 = 1
@@ -149,6 +158,22 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd_varlen.restype = ctypes.c_int
             L.fa_bwd_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32]
             L.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
+            i32, f32, ptr = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
+            L.fa_fwd_shared_prefix.argtypes = [P(Tensor)] * 10 + [f32, i32, i32, P(ScoreMod), P(SharedPrefix), i32,
+                                                                 P(Launch), ptr]
+            L.fa_fwd_shared_prefix.restype = ctypes.c_int
+            L.fa_shared_prefix_plan_create.argtypes = L.fa_fwd_shared_prefix.argtypes[:-1] + [P(ptr)]
+            L.fa_shared_prefix_plan_create.restype = ctypes.c_int
+            L.fa_shared_prefix_workspace_bytes.argtypes = [P(Launch), P(SharedPrefix), i32, i32]
+            L.fa_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
+            L.fa_shared_prefix_default_splits.argtypes = [ctypes.c_int64, i32, i32, i32, i32]
+            L.fa_shared_prefix_default_splits.restype = i32
+            L.fa_key_weights.argtypes = [P(Tensor)] * 8 + [f32, P(Tensor), f32, i32, i32, P(ScoreMod), i32, P(Launch), ptr]
+            L.fa_key_weights.restype = ctypes.c_int
+            L.fa_key_weights_plan_create.argtypes = L.fa_key_weights.argtypes[:-1] + [P(ptr)]
+            L.fa_key_weights_plan_create.restype = ctypes.c_int
+            L.fa_cache_evict.argtypes = [P(Tensor)] * 11 + [i32] * 4 + [P(Launch), ptr]
+            L.fa_cache_evict.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -467,3 +492,240 @@ def bwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
                            int(window), ctypes.byref(sm), _ref(bm), ctypes.byref(launch),
                            ctypes.c_void_p(_stream_ptr(stream))))
     return dq, dk, dv
+
+
+# ------------------------------------------------- around the paged decode --
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Make ``device`` and ``stream`` (None: the device's current stream)
+    current, so that what a call allocates belongs to the stream it runs on;
+    yields the stream's handle."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not {device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _same_device(device: torch.device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, one is on {t.device}")
+
+
+class _Prepared:
+    """A prepared call behind ``fa_fwd_plan_launch``: run() enqueues it."""
+
+    def __init__(self, device, keep, result, handle):
+        L = lib()
+        self._device = device
+        self._keep = keep
+        self._result = result
+        self._plan = handle
+        self._launch_fn = L.fa_fwd_plan_launch
+        self._destroy_fn = L.fa_fwd_plan_destroy
+
+    def run(self, stream=None):
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        if torch.cuda.current_device() == self._device.index:
+            st = self._launch_fn(self._plan, ctypes.c_void_p(stream.cuda_stream))
+        else:
+            with torch.cuda.device(self._device):
+                st = self._launch_fn(self._plan, ctypes.c_void_p(stream.cuda_stream))
+        if st != FA_OK:
+            _check(st)
+        return self._result
+
+    def __del__(self):
+        plan = getattr(self, "_plan", None)
+        if plan is not None and plan.value:
+            self._destroy_fn(plan)
+            self._plan = None
+
+
+def shared_prefix_default_splits(total_q: int, num_groups: int, max_prefix_len: int, hq: int, hkv: int) -> int:
+    return int(lib().fa_shared_prefix_default_splits(int(total_q), num_groups, max_prefix_len, hq, hkv))
+
+
+def shared_prefix_workspace_bytes(launch: "Launch", prefix: "SharedPrefix", hq: int, dv: int) -> int:
+    return int(lib().fa_shared_prefix_workspace_bytes(ctypes.byref(launch), ctypes.byref(prefix), hq, dv))
+
+
+def _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q, max_seqlen_k, block_table,
+                        page_size, cu_groups, prefix_lens, max_prefix_len, total_k=None, k_scale=None, v_scale=None,
+                        softmax_scale=None, causal=False, window=0, score_mod=MOD_NONE, alibi_slope=0.0, softcap=0.0,
+                        prefix_splits=None, num_splits=None, out=None, lse=None, return_lse=True, workspace=None):
+    """The C arguments up to the launch, what they point at, and (out, lse)."""
+    B = cu_seqlens_q.shape[0] - 1
+    Tq, Hq, D = q.shape
+    Hkv, Dv = _cache_dims(k_cache, v_cache)
+    kv_dt = _kv_dtype(k_cache)
+    _same_device(q.device, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_table, cu_groups, prefix_lens, k_scale,
+                 v_scale, out, lse, workspace)
+    for name, t, n in (("cu_groups", cu_groups, None), ("prefix_lens", prefix_lens, cu_groups.shape[0] - 1)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+            raise ValueError(f"{name} must be contiguous int32: cu_groups [G + 1], prefix_lens [G]")
+    if out is None:
+        out = torch.empty((Tq, Hq, Dv), dtype=torch.bfloat16, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    groups = cu_groups.shape[0] - 1
+    if prefix_splits is None:
+        prefix_splits = shared_prefix_default_splits(Tq, groups, max_prefix_len, Hq, Hkv)
+    if num_splits is None:
+        own = max(0, total_k - B * max_prefix_len) if total_k is not None else 0
+        num_splits = max(1, default_splits(B, max_seqlen_q, max(0, max_seqlen_k - max_prefix_len), Hq, Hkv, page_size,
+                                           own))
+    launch = Launch(num_seqs=B, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
+                    total_q=Tq, total_k=0)
+    prefix = SharedPrefix(cu_groups=cu_groups.data_ptr(), lens=prefix_lens.data_ptr(), num_groups=groups,
+                          max_len=max_prefix_len, num_splits=prefix_splits)
+    need = shared_prefix_workspace_bytes(launch, prefix, Hq, Dv)
+    if need:
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        launch.workspace = workspace.data_ptr()
+        launch.workspace_bytes = workspace.numel() * workspace.element_size()
+    sm = ScoreMod(kind=score_mod, alibi_slope=alibi_slope, softcap=softcap)
+    descs = [as_tensor(q), as_tensor(k_cache, kv_dt), as_tensor(v_cache, kv_dt), as_tensor(block_table),
+             as_tensor(cu_seqlens_q), as_tensor(cu_seqlens_k), as_tensor(k_scale), as_tensor(v_scale), as_tensor(out),
+             as_tensor(lse)]
+    args = [_ref(a) for a in descs] + [float(softmax_scale), int(bool(causal)), int(window), ctypes.byref(sm),
+                                       ctypes.byref(prefix), int(page_size), ctypes.byref(launch)]
+    keep = [q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_table, cu_groups, prefix_lens, k_scale, v_scale, out,
+            lse, workspace]
+    return args, keep, (out, lse)
+
+
+def fwd_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                      cu_seqlens_k: torch.Tensor, *, stream=None, **kw):
+    """Paged decode of a batch whose sequences share prefixes, through
+    ``fa_fwd_shared_prefix``: the result of ``fwd_varlen`` on the same
+    arguments, with each shared prefix read once.
+
+    q [T_q, Hq, D] bf16 (D 64 or 128, max_seqlen_q * Hq/Hkv <= 16); k_cache and
+    v_cache [N_pg, P_s, Hkv, D] (bf16, or e4m3 / int8 with k_scale, v_scale).
+    Keywords: max_seqlen_q, max_seqlen_k, block_table [B, max_pages], page_size;
+    ``cu_groups`` int32 [G + 1], the sequences of each group; ``prefix_lens``
+    int32 [G], how many first keys the sequences of a group hold in the same
+    pages (rounded down to whole pages; counted in cu_seqlens_k);
+    ``max_prefix_len``, a host bound on prefix_lens; optional total_k (host sum
+    of key lengths), k_scale, v_scale, softmax_scale, causal, window, score_mod,
+    alibi_slope, softcap, out, lse, return_lse, workspace, and the split counts
+    prefix_splits and num_splits (None: the library's choice).  Returns
+    ``(out [T_q, Hq, D] bf16, lse [Hq, T_q] fp32 or None)``."""
+    with _on(q.device, stream) as s:
+        args, _keep, result = _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw)
+        _check(lib().fa_fwd_shared_prefix(*args, s))
+    return result
+
+
+class SharedPrefixPlan(_Prepared):
+    """A prepared fwd_shared_prefix call (same arguments): run() only enqueues
+    its kernels and returns (out, lse).  The tensors must stay alive, unmoved
+    and of the same shape; lengths, tables and group sizes are read at each
+    run.  Two runs at once on different streams would race on the workspace."""
+
+    def __init__(self, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw):
+        with _on(q.device, None):
+            args, keep, result = _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw)
+            handle = ctypes.c_void_p(0)
+            _check(lib().fa_shared_prefix_plan_create(*args, ctypes.byref(handle)))
+            super().__init__(q.device, keep, result, handle)
+
+
+def _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q, max_seqlen_k, weights=None, beta=1.0,
+                      out=None, block_table=None, page_size=0, total_k=None, k_scale=None, softmax_scale=None,
+                      causal=False, window=0, score_mod=MOD_NONE, alibi_slope=0.0, softcap=0.0):
+    B = cu_seqlens_q.shape[0] - 1
+    Tq, _Hq, D = q.shape
+    _same_device(q.device, k_cache, lse, cu_seqlens_q, cu_seqlens_k, weights, out, block_table, k_scale)
+    if out is None:
+        out = weights
+    if out is None:
+        out = torch.empty((B, k_cache.shape[-2], max_seqlen_k), dtype=torch.float32, device=q.device)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if total_k is None:
+        total_k = k_cache.shape[0] if block_table is None else 0
+    launch = Launch(num_seqs=B, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, num_splits=0, total_q=Tq,
+                    total_k=total_k)
+    sm = ScoreMod(kind=score_mod, alibi_slope=alibi_slope, softcap=softcap)
+    descs = [as_tensor(q), as_tensor(k_cache, _kv_dtype(k_cache)), as_tensor(block_table), as_tensor(cu_seqlens_q),
+             as_tensor(cu_seqlens_k), as_tensor(k_scale), as_tensor(lse), as_tensor(weights)]
+    args = [_ref(a) for a in descs] + [float(beta), ctypes.byref(as_tensor(out)), float(softmax_scale),
+                                       int(bool(causal)), int(window), ctypes.byref(sm), int(page_size),
+                                       ctypes.byref(launch)]
+    return args, [q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, weights, out, block_table, k_scale], out
+
+
+def key_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                cu_seqlens_k: torch.Tensor, *, stream=None, **kw):
+    """The attention weight each key received, through ``fa_key_weights``:
+    ``out[b, hk, j] = beta * weights[b, hk, j] + sum exp(s_ij - lse[h, i])`` over
+    the rows of sequence b and the heads of group hk that see key j.
+
+    q [T_q, Hq, Dk] bf16 (Dk 64, 128 or 192); k_cache packed [T_k, Hkv, Dk] or
+    paged [N_pg, P_s, Hkv, Dk] (bf16, or e4m3 / int8 with k_scale); ``lse`` the
+    forward's fp32 [Hq, T_q].  Keywords: max_seqlen_q, max_seqlen_k;
+    ``weights`` fp32 [B, Hkv, L] or None (start from 0), ``beta`` (default 1),
+    ``out`` (default: ``weights``, updated in place, or a new [B, Hkv,
+    max_seqlen_k]); block_table and page_size for paged keys; total_k, k_scale,
+    softmax_scale, causal, window, score_mod, alibi_slope, softcap as in the
+    forward call that wrote ``lse``.  Returns ``out``."""
+    with _on(q.device, stream) as s:
+        args, _keep, out = _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw)
+        _check(lib().fa_key_weights(*args, s))
+    return out
+
+
+class KeyWeightsPlan(_Prepared):
+    """A prepared key_weights call (same arguments), as SharedPrefixPlan; run()
+    returns out."""
+
+    def __init__(self, q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw):
+        with _on(q.device, None):
+            args, keep, out = _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw)
+            handle = ctypes.c_void_p(0)
+            _check(lib().fa_key_weights_plan_create(*args, ctypes.byref(handle)))
+            super().__init__(q.device, keep, out, handle)
+
+
+def cache_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens_k: torch.Tensor, *,
+                block_table: torch.Tensor, page_size: int, budget: int, sink: int = 0, recent: int = 0,
+                max_seqlen_k: int, k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                block_table_out: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                kept: Optional[torch.Tensor] = None, cu_seqlens_k_out: Optional[torch.Tensor] = None, stream=None):
+    """Shorten the sequences of a paged cache to ``budget`` keys per kv head
+    through ``fa_cache_evict``: a longer sequence keeps its first ``sink`` keys,
+    its last ``recent`` and the others of largest weight, in their order.
+
+    ``weights`` fp32 [B, Hkv, L] (key_weights); the K and V rows, scales and
+    weights of the kept keys move to keys 0 ... n - 1, in the same pages or in
+    those of ``block_table_out``; weights past them become 0 (``weights_out``:
+    write the weights there instead of in place).  Returns ``(kept int32 [B,
+    Hkv, budget]: old indices, -1 past the kept keys; cu_seqlens_k_out int32
+    [B + 1])``."""
+    B, Hkv = weights.shape[0], weights.shape[1]
+    _same_device(weights.device, k_cache, v_cache, cu_seqlens_k, block_table, k_scale, v_scale, block_table_out,
+                 weights_out, kept, cu_seqlens_k_out)
+    with _on(weights.device, stream) as s:
+        if kept is None:
+            kept = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
+        if cu_seqlens_k_out is None:
+            cu_seqlens_k_out = torch.empty((B + 1,), dtype=torch.int32, device=weights.device)
+        kv_dt = _kv_dtype(k_cache)
+        launch = Launch(num_seqs=B, max_seqlen_q=0, max_seqlen_k=max_seqlen_k)
+        descs = [as_tensor(weights), as_tensor(weights_out), as_tensor(k_cache, kv_dt), as_tensor(v_cache, kv_dt),
+                 as_tensor(k_scale), as_tensor(v_scale), as_tensor(block_table), as_tensor(block_table_out),
+                 as_tensor(cu_seqlens_k), as_tensor(cu_seqlens_k_out), as_tensor(kept)]
+        _check(lib().fa_cache_evict(*[_ref(d) for d in descs], int(budget), int(sink), int(recent), int(page_size),
+                                    ctypes.byref(launch), s))
+    return kept, cu_seqlens_k_out

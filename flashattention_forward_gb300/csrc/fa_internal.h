@@ -8,6 +8,9 @@
 #include "fa_decode.cuh"
 #include "fa_prefill.cuh"
 #include "fa_bwd_params.h"
+#include "fa_evict.cuh"
+#include "fa_key_weights.cuh"
+#include "fa_prefix.cuh"
 
 namespace fa {
 
@@ -108,6 +111,36 @@ cudaError_t launch_decode(int d, const DecodeLaunch &L);
 cudaError_t launch_combine(const float *o_part, const float *lse_part, int num_splits, int64_t n_rows, int hq,
                            int dv, void *out, float *lse, cudaStream_t stream);
 
+// Shared-prefix decode: the prefix pass of all groups (fa_prefix.cuh), the
+// decode of each sequence's own keys, and the merge of their partials.
+struct PrefixLaunch {
+  CUtensorMap tm_q, tm_k, tm_v;
+  PrefixParams p;
+  int kv, mod;     // cache: 0 bf16, 1 e4m3, 2 int8; score mod as PrefixParams' kernel takes it
+  dim3 grid;
+  cudaStream_t stream;
+};
+cudaError_t launch_prefix(int d, const PrefixLaunch &L);
+// Merge of num_splits partials, one warp per (row, head).
+cudaError_t launch_prefix_merge(int d, const float *o_part, const float *lse_part, const int32_t *cu_q, int num_seqs,
+                                int num_splits, int64_t n_rows, int hq, void *out, float *lse, cudaStream_t stream);
+cudaError_t launch_decode_suffix(int d, const DecodeLaunch &L);
+
+struct KeyWeightsLaunch {
+  CUtensorMap tm_q;
+  KeyWeightsParams p;
+  int row_tiles;   // rows form with this many tiles of 8 rows; 0: tile form
+  dim3 grid;
+  cudaStream_t stream;
+};
+cudaError_t launch_key_weights(int d, const KeyWeightsLaunch &L);
+
+struct EvictLaunch {
+  EvictParams p;
+  cudaStream_t stream;
+};
+cudaError_t launch_evict(const EvictLaunch &L);
+
 // Records a host-side error message for fa_last_error() and returns `st`.
 fa_status_t set_host_error(fa_status_t st, const char *msg);
 
@@ -128,4 +161,31 @@ cudaError_t ensure_smem_attr(K kernel, int bytes, unsigned long long *done_mask)
   return e;
 }
 
+}  // namespace fa
+
+// A prepared forward call (fa_fwd_plan_create): the launch descriptors that
+// fa_fwd_varlen would enqueue, kept for repeated launches.
+struct fa_fwd_plan_s {
+  // 0: nothing to launch, 1: split-KV decode (+ combine), 2: prefill,
+  // 3: shared-prefix decode, 4: key weights, 5: cache eviction
+  int kind = 0;
+  int device = -1;           // kinds 3 to 5: the device current at creation
+  int dk = 0, fp8 = 0;
+  int has_cb = 0;            // the prologue's per-key term is computed first
+  fa::ColBiasParams cb;
+  int has_vm = 0;            // e4m3 P * V: the V-scale maxima are computed first
+  fa::VmaxParams vm;
+  fa::DecodeLaunch dl;
+  int splits = 0, hq = 0, dv = 0;
+  int64_t rows = 0;
+  void *out = nullptr;
+  fa::PrefillLaunch pl;
+  fa::PrefixLaunch px;       // kind 3, with dl (the sequences' own keys) and splits (of both passes)
+  fa::KeyWeightsLaunch kw;
+  fa::EvictLaunch ev;
+};
+
+namespace fa {
+// Enqueues a plan of kind 3 to 5 (fa_serving.cu).
+fa_status_t run_serving(const fa_fwd_plan_s &P, cudaStream_t stream);
 }  // namespace fa

@@ -1,0 +1,599 @@
+// fa_key_weights.cuh -- the attention weight that each cached key received:
+//
+//   w_out[b][hk][j] = beta * w_in[b][hk][j]
+//                     + sum_{rows i of b, heads h of group hk} exp(s_ij - LSE[h][i])
+//
+// over the (i, j) that the masks allow, from the forward's saved LSE: the
+// column sums of the attention matrix, which the forward itself never forms.
+// V is not read, and the softmax needs no running statistics, so the keys can
+// be cut anywhere without a merge.
+//
+// Rows form (few query rows per kv head: decode and drafts).  Bound by
+// reading K once.  The keys go from global memory straight into the A
+// fragments of S^T = K Q^T (mma.sync as a dense FMA engine, as in the split-KV
+// decode): the contraction index is permuted so that a lane's 16-byte piece of
+// a key row is what the lane's fragments hold, hence no shared memory, no
+// barrier, and any page size costs one page-table read per key row.
+//
+// Tile form (prompts).  Bound by the QK product and one exponential per pair:
+// S^T tiles of 128 keys x 128 query rows on tcgen05 with fp32 accumulators in
+// TMEM.  A CTA keeps its 128 keys as the A operand and streams the query rows
+// of its kv head -- (token, head of the group) packed into one tile by a
+// three-dimensional TMA box -- as B.  A thread owns a key, so a column sum is a
+// sum in one register: no shuffles, no atomics, the same result every run.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <climits>
+
+#include "fa_decode.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+struct KeyWeightsParams {
+  const __nv_bfloat16 *q;
+  int64_t q_stride_t, q_stride_h;     // elements
+  const int32_t *cu_q, *cu_k;
+  const int32_t *block_table;         // null: packed
+  int64_t bt_stride, max_pages;
+  int32_t page_size, page_shift;
+  int64_t n_pages;                    // pages in the pool (packed: rows of the cache)
+  const uint8_t *k;
+  int64_t s_page, s_slot, s_head;     // bytes: page (packed: token row), slot, kv head
+  const float *k_scale;               // byte caches: per (token, kv head)
+  const float *lse;                   // [Hq, T_q]
+  int64_t total_q;
+  const float *w_in;                  // null: beta is 0
+  int64_t wi_stride_b, wi_stride_h;
+  float *w_out;
+  int64_t wo_stride_b, wo_stride_h;
+  int64_t extent;                     // entries per (sequence, kv head) row of w_out
+  int64_t max_keys;                   // the host's bound on a sequence's keys
+  float beta;
+  int32_t inplace;                    // w_out is w_in and beta is 1: entries that gain nothing stay untouched
+  int32_t hq, hkv, group;
+  int32_t kv;                         // 0 bf16, 1 e4m3, 2 int8
+  int32_t mod, causal, window;
+  float scale_log2, alibi_log2, softcap_arg, softcap_log2;
+  int32_t keys_per_cta;               // rows form
+  int32_t tokens_per_tile;            // tile form: 128 / group
+  int *err;
+};
+
+// The lengths of one sequence, with the key count held to what the weights
+// and the page table cover (a longer sequence is flagged).
+struct KwSeq {
+  int qa, sq, ka, sk, shift;          // shift = Sk - Sq: i' = i + shift
+};
+__device__ __forceinline__ KwSeq kw_sequence(const KeyWeightsParams &p, int b) {
+  KwSeq s;
+  s.qa = __ldg(p.cu_q + b);
+  s.sq = __ldg(p.cu_q + b + 1) - s.qa;
+  s.ka = __ldg(p.cu_k + b);
+  const int sk = __ldg(p.cu_k + b + 1) - s.ka;
+  s.shift = sk - s.sq;
+  int64_t cap = min(p.extent, p.max_keys);
+  if (p.block_table) cap = min(cap, p.max_pages * p.page_size);
+  if (sk > cap && threadIdx.x == 0) record_error(p.err, kErrBounds);
+  s.sk = (int)min((int64_t)sk, cap);
+  return s;
+}
+
+// Row of the flat [tokens, Hkv] cache view that holds key j; -1 (flagged) for
+// a page or row outside the cache.
+__device__ __forceinline__ int64_t kw_token(const KeyWeightsParams &p, int b, const KwSeq &s, int j, const uint8_t *&row,
+                                            int hk) {
+  int64_t tok;
+  if (p.block_table) {
+    const int page = __ldg(p.block_table + (int64_t)b * p.bt_stride + (j >> p.page_shift));
+    const int slot = j & (p.page_size - 1);
+    if (page < 0 || page >= p.n_pages) {
+      record_error(p.err, kErrBounds);
+      return -1;
+    }
+    tok = (int64_t)page * p.page_size + slot;
+    row = p.k + (int64_t)page * p.s_page + (int64_t)slot * p.s_slot + (int64_t)hk * p.s_head;
+  } else {
+    tok = (int64_t)s.ka + j;
+    if (tok < 0 || tok >= p.n_pages) {
+      record_error(p.err, kErrBounds);
+      return -1;
+    }
+    row = p.k + tok * p.s_page + (int64_t)hk * p.s_head;
+  }
+  return tok;
+}
+
+// Entries [lo, hi) that gain nothing: w_out = beta * w_in.
+__device__ __forceinline__ void kw_carry(const KeyWeightsParams &p, int b, int hk, int64_t lo, int64_t hi) {
+  if (p.inplace) return;
+  const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
+  float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
+  for (int64_t j = lo + threadIdx.x; j < hi; j += blockDim.x) wo[j] = wi ? p.beta * wi[j] : 0.f;
+}
+
+__device__ __forceinline__ uint4 kw_ld_stream(const uint8_t *a) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(a));
+  return v;
+}
+
+// exp2 argument of one pair from the raw product s, factor c (scale, key
+// scale and row factor, in log2 units; soft-cap: in 2u log2(e) units).
+__device__ __forceinline__ float kw_score(const KeyWeightsParams &p, float s, float c, int dist) {
+  if (p.mod == 2) {
+    float r;
+    return softcap_log2_score(ex2(s * c), p.softcap_log2, r);
+  }
+  if (p.mod == 1) return fmaf(s, c, -p.alibi_log2 * fabsf((float)dist));
+  return s * c;
+}
+
+// --------------------------------------------------------------- rows form --
+constexpr int kKwWarps = 8;
+
+// NT tiles of 8 query rows.
+template <int D, int KV, int NT>
+__global__ void __launch_bounds__(kKwWarps * 32) fa_key_weights_rows_kernel(const KeyWeightsParams p) {
+  constexpr int ESZ = KV ? 1 : 2;
+  constexpr int NP = D * ESZ / 64;            // 16-byte pieces of a key row per lane
+  constexpr int U = NP * 4 <= 16 ? 2 : 1;     // 16-key groups per warp step: up to 64 registers of keys in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const KwSeq sq_ = kw_sequence(p, b);
+  const int64_t lo64 = (int64_t)blockIdx.x * p.keys_per_cta;
+  const int64_t hi64 = min(p.extent, lo64 + p.keys_per_cta);
+  int rows = sq_.sq * p.group;
+  if (rows > NT * 8) {
+    if (threadIdx.x == 0) record_error(p.err, kErrBounds);
+    rows = NT * 8;
+  }
+  if (rows <= 0 || lo64 >= sq_.sk) {
+    kw_carry(p, b, hk, lo64, hi64);
+    return;
+  }
+  const int lo = (int)lo64, hi = (int)min(hi64, (int64_t)sq_.sk);
+  kw_carry(p, b, hk, hi, hi64);
+
+  // Query rows as B fragments (k16 x n8): row 8 nt + g, the lane's pieces.
+  uint32_t qb[D / 16][NT][2];
+  float inv[NT];                              // byte caches: 2^-e of row 8 nt + g
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g;
+    const bool live = r < rows;
+    const __nv_bfloat16 *src = p.q;
+    if (live)
+      src = p.q + (int64_t)(sq_.qa + r / p.group) * p.q_stride_t + (int64_t)(hk * p.group + r % p.group) * p.q_stride_h;
+    inv[nt] = 1.f;
+    if constexpr (KV == 0) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * (t + 4 * i))) : make_uint4(0, 0, 0, 0);
+        qb[2 * i][nt][0] = v.x;
+        qb[2 * i][nt][1] = v.y;
+        qb[2 * i + 1][nt][0] = v.z;
+        qb[2 * i + 1][nt][1] = v.w;
+      }
+    } else {
+      // f16 with a power-of-two factor per row, max|q| 2^e in [2^14, 2^15):
+      // bf16 values within 2^-24 of the row's largest are exact
+      uint4 v[2 * NP];
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          v[2 * i + u] =
+              live ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * i) + 8 * u)) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[2 * i + u].x, v[2 * i + u].y, v[2 * i + u].z, v[2 * i + u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int sh = 0;
+      if (mx > 0.f && mx <= 3.0e38f) sh = min(141 - (int)((__float_as_uint(mx) >> 23) & 0xFF), 126);
+      const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
+      inv[nt] = __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+      for (int i = 0; i < 2 * NP; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
+        qb[2 * i][nt][0] = h[0];
+        qb[2 * i][nt][1] = h[1];
+        qb[2 * i + 1][nt][0] = h[2];
+        qb[2 * i + 1][nt][1] = h[3];
+      }
+    }
+  }
+  // The rows of this lane's C columns, 8 nt + 2t + e: -LSE (log2 units), i',
+  // and the score factor.  Rows that see nothing (LSE -inf) weigh nothing.
+  float nl[NT][2], sc[NT][2];
+  int ip[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * t + e;
+      const float f = __shfl_sync(0xffffffffu, inv[nt], (2 * t + e) * 4);
+      sc[nt][e] = (p.mod == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * f;
+      nl[nt][e] = -INFINITY;
+      ip[nt][e] = 0;
+      if (r < rows) {
+        const float l = __ldg(p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + sq_.qa + r / p.group);
+        nl[nt][e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        ip[nt][e] = r / p.group + sq_.shift;
+      }
+    }
+
+  const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
+  float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
+  for (int base = lo + warp * 16 * U; base < hi; base += kKwWarps * 16 * U) {
+    uint4 kr[2 * U][NP];
+    float ks[2 * U];
+    bool live[2 * U];
+#pragma unroll
+    for (int u = 0; u < 2 * U; ++u) {         // the lane's key rows: base + 8 u + g
+      const int j = base + 8 * u + g;
+      const uint8_t *row = p.k;
+      int64_t tok = -1;
+      if (j < hi) tok = kw_token(p, b, sq_, j, row, hk);
+      live[u] = tok >= 0;
+      ks[u] = (KV && live[u]) ? __ldg(p.k_scale + tok * p.hkv + hk) : 1.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kr[u][i] = live[u] ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float c[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint32_t w0[4] = {kr[2 * u][i].x, kr[2 * u][i].y, kr[2 * u][i].z, kr[2 * u][i].w};
+        const uint32_t w1[4] = {kr[2 * u + 1][i].x, kr[2 * u + 1][i].y, kr[2 * u + 1][i].z, kr[2 * u + 1][i].w};
+        if constexpr (KV == 0) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t a[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(c[nt], a, qb[2 * i + s][nt][0], qb[2 * i + s][nt][1]);
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t a[4];
+            dec_bytes4_to_f16<KV>(w0[s], a[0], a[2]);
+            dec_bytes4_to_f16<KV>(w1[s], a[1], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(c[nt], a, qb[4 * i + s][nt][0], qb[4 * i + s][nt][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {           // keys base + 16 u + 8 x + g
+        const int j = base + 16 * u + 8 * x + g;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int d = ip[nt][e] - j;
+            bool vis = live[2 * u + x] && nt * 8 + 2 * t + e < rows;
+            if (p.causal) vis = vis && d >= 0;
+            if (p.window > 0) vis = vis && (p.causal ? d < p.window : abs(d) < p.window);
+            const float y = kw_score(p, c[nt][2 * x + e], sc[nt][e] * ks[2 * u + x], d) + nl[nt][e];
+            sum += vis ? ex2(y) : 0.f;
+          }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (t == 0 && j < hi) wo[j] = wi ? fmaf(p.beta, wi[j], sum) : sum;
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------- tile form --
+template <int D>
+struct KwTileCfg {
+  static constexpr int KC = D / 64;                 // 64-column blocks
+  static constexpr int kChunkBytes = 128 * 128;
+  static constexpr int NCH = D == 192 ? 3 : 4;      // Q ring, in blocks; two CTAs per SM
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = KC * kChunkBytes;
+  static constexpr int kOffCol = kOffQ + NCH * kChunkBytes;   // [2][128] -LSE, [2][128] i'
+  static constexpr int kOffBar = kOffCol + 2 * 128 * 8;
+  static constexpr int kSmemBytes = kOffBar + (2 * NCH + 4) * 8 + 16 + 1024;
+  static constexpr int kThreads = 6 * 32;
+  static constexpr uint32_t kTmemCols = 256;        // two S^T tiles
+  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+};
+
+// Eight e4m3 or int8 bytes -> eight bf16 (exact: both have at most 8
+// significant bits).
+template <int KV>
+__device__ __forceinline__ uint4 kw_bytes8_to_bf16(uint2 w) {
+  uint32_t h[4], o[4];
+  dec_bytes4_to_f16<KV>(w.x, h[0], h[1]);
+  dec_bytes4_to_f16<KV>(w.y, h[2], h[3]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+    o[e] = pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int D, int MOD>
+__global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
+    fa_key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const KeyWeightsParams p) {
+  using Cfg = KwTileCfg<D>;
+  constexpr int KC = Cfg::KC, NCH = Cfg::NCH;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const KwSeq s = kw_sequence(p, b);
+  const int64_t j0_64 = (int64_t)blockIdx.x * 128;
+  if (s.sq <= 0 || j0_64 >= s.sk) {
+    kw_carry(p, b, hk, j0_64, min(p.extent, j0_64 + 128));
+    return;
+  }
+  const int j0 = (int)j0_64;
+  const int jl = min(j0 + 128, s.sk) - 1;           // last key of the tile
+  // tokens [t_lo, t_hi) that see a key of the tile
+  int t_lo = 0, t_hi = s.sq;
+  if (p.causal) t_lo = max(t_lo, j0 - s.shift);
+  if (p.window > 0) {
+    t_hi = min(t_hi, jl + p.window - s.shift);                         // i' - j < window for some j
+    if (!p.causal) t_lo = max(t_lo, j0 - p.window + 1 - s.shift);      // j - i' < window
+  }
+  const int tpt = p.tokens_per_tile;
+  const int n_tiles = t_hi > t_lo ? (t_hi - t_lo + tpt - 1) / tpt : 0;
+  if (n_tiles == 0) {
+    kw_carry(p, b, hk, j0, min(p.extent, j0_64 + 128));
+    return;
+  }
+  uint8_t *sK = smem + Cfg::kOffK, *sQ = smem + Cfg::kOffQ;
+  float *col_nl = reinterpret_cast<float *>(smem + Cfg::kOffCol);      // [2][128]
+  int *col_ip = reinterpret_cast<int *>(col_nl + 256);                 // [2][128]
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
+  uint64_t *q_empty = q_full + NCH, *s_full = q_empty + NCH, *s_empty = s_full + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_empty + 2);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int rows_box = tpt * p.group;               // rows of a Q tile, at most 128
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NCH; ++i) {
+      mbar_init(smem_u32(q_full + i), 1);
+      mbar_init(smem_u32(q_empty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(s_empty + i), 128);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  // rows that no box writes (128 % group != 0) stay zero
+  for (int e = threadIdx.x; e < NCH * (128 - rows_box) * 8; e += Cfg::kThreads) {
+    const int ch = e / ((128 - rows_box) * 8), rest = e % ((128 - rows_box) * 8);
+    *reinterpret_cast<uint4 *>(sQ + ch * Cfg::kChunkBytes + rows_box * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+  }
+  // The key tile as the K-major, 128-byte-swizzled A operand in bf16: any page
+  // size, and byte caches exactly (their scale multiplies the key's sum
+  // argument below).  Rows past the sequence are zero.
+  if (p.kv == 0) {
+    constexpr int PR = D / 8;                       // 16-byte pieces of a row
+    for (int e = threadIdx.x; e < 128 * PR; e += Cfg::kThreads) {
+      const int r = e / PR, c = e % PR, j = j0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const uint8_t *row;
+      if (j < s.sk && kw_token(p, b, s, j, row, hk) >= 0) v = kw_ld_stream(row + c * 16);
+      *reinterpret_cast<uint4 *>(sK + (c >> 3) * Cfg::kChunkBytes + sw128(r, c & 7)) = v;
+    }
+  } else {
+    constexpr int PR = D / 16;
+    for (int e = threadIdx.x; e < 128 * PR; e += Cfg::kThreads) {
+      const int r = e / PR, c = e % PR, j = j0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const uint8_t *row;
+      if (j < s.sk && kw_token(p, b, s, j, row, hk) >= 0) v = kw_ld_stream(row + c * 16);
+      const uint2 lo = make_uint2(v.x, v.y), hi = make_uint2(v.z, v.w);
+      uint8_t *dst = sK + (c >> 2) * Cfg::kChunkBytes;
+      const int c8 = (2 * c) & 7;
+      *reinterpret_cast<uint4 *>(dst + sw128(r, c8)) = p.kv == 1 ? kw_bytes8_to_bf16<1>(lo) : kw_bytes8_to_bf16<2>(lo);
+      *reinterpret_cast<uint4 *>(dst + sw128(r, c8 + 1)) =
+          p.kv == 1 ? kw_bytes8_to_bf16<1>(hi) : kw_bytes8_to_bf16<2>(hi);
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    // ------------------------------------------------------- producer --
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      const uint32_t bytes = (uint32_t)rows_box * 128u;
+      int n = 0;
+      bool ok = true;
+      for (int it = 0; ok && it < n_tiles; ++it)
+        for (int c = 0; c < KC; ++c, ++n) {
+          const int slot = n % NCH;
+          if (n >= NCH && !(ok = mbar_wait(smem_u32(q_empty + slot), ((n / NCH) - 1) & 1, abort_flag, p.err))) break;
+          mbar_expect_tx(smem_u32(q_full + slot), bytes);
+          tma_load_3d(smem_u32(sQ + slot * Cfg::kChunkBytes), &tm_q, smem_u32(q_full + slot), c * 64, hk * p.group,
+                      s.qa + t_lo + it * tpt);
+        }
+      // the last loads have landed before the CTA ends, whatever the others do
+      for (int i = max(0, n - NCH); i < n; ++i) mbar_wait(smem_u32(q_full + i % NCH), (i / NCH) & 1, abort_flag, p.err);
+    }
+  } else if (warp == 5) {
+    // ----------------------------------------------------------- MMAs --
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+      const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint32_t hi = (uint32_t)(dk >> 32), lo_k = (uint32_t)dk;
+      const uint32_t lo_q = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      int n = 0;
+      bool ok = true;
+      for (int it = 0; ok && it < n_tiles; ++it) {
+        const int x = it & 1;
+        if (it >= 2 && !(ok = mbar_wait(smem_u32(s_empty + x), ((it >> 1) - 1) & 1, abort_flag, p.err))) break;
+        const uint32_t d = tmem + x * 128u;
+        for (int c = 0; c < KC; ++c, ++n) {
+          const int slot = n % NCH;
+          if (!(ok = mbar_wait(smem_u32(q_full + slot), (n / NCH) & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          uint32_t a = lo_k + (uint32_t)(c * (Cfg::kChunkBytes >> 4)), q = lo_q + (uint32_t)(slot * (Cfg::kChunkBytes >> 4));
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            if (ks == 0 && c == 0) mma_ss_w<0>(d, a, hi, q, hi, idesc);
+            else mma_ss_w<1>(d, a, hi, q, hi, idesc);
+            a += 2;
+            q += 2;
+          }
+          tc_commit(smem_u32(q_empty + slot));
+        }
+        if (!ok) break;
+        tc_commit(smem_u32(s_full + x));
+      }
+    }
+  } else {
+    // --------------------------------------------- one key per thread --
+    const int r = threadIdx.x, j = j0 + r;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    float ks = 1.f;
+    if (p.kv && j < s.sk) {
+      const uint8_t *row;
+      const int64_t tok = kw_token(p, b, s, j, row, hk);
+      if (tok >= 0) ks = __ldg(p.k_scale + tok * p.hkv + hk);
+    }
+    const float c = (MOD == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * ks;
+    // column r of a tile: token t_lo + it * tpt + r / group, head r % group
+    const int ctok = r / p.group;
+    const float *lse_r = p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + s.qa;
+    auto column = [&](int it, float &nl, int &ip) {
+      const int tok = t_lo + it * tpt + ctok;
+      nl = -INFINITY;
+      ip = INT_MIN / 2;                             // hidden from every key
+      if (it < n_tiles && r < rows_box && tok < t_hi) {
+        const float l = __ldg(lse_r + tok);
+        nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        ip = tok + s.shift;
+      }
+    };
+    float nl_next;
+    int ip_next;
+    column(0, nl_next, ip_next);
+    float total = 0.f;
+    bool ok = true;
+    for (int it = 0; it < n_tiles; ++it) {
+      const int x = it & 1;
+      // this tile's column constants; the buffer's last readers passed the
+      // previous tile's barrier
+      col_nl[x * 128 + r] = nl_next;
+      col_ip[x * 128 + r] = ip_next;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      column(it + 1, nl_next, ip_next);
+      const int ta = t_lo + it * tpt, tb = min(ta + tpt, t_hi) - 1;    // first and last token of the tile
+      bool mask = tb - ta + 1 < tpt;                 // rows of other sequences may hold anything
+      if (p.causal) mask = mask || ta + s.shift < jl;
+      if (p.window > 0) mask = mask || tb + s.shift - j0 >= p.window || (!p.causal && jl - ta - s.shift >= p.window);
+      ok = mbar_wait(smem_u32(s_full + x), (it >> 1) & 1, abort_flag, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[32];
+        tmem_ld32(tmem + lane_base + x * 128u + q * 32u, v);
+        tmem_wait_ld();
+        if (q == 3) {
+          tc_fence_before();
+          mbar_arrive(smem_u32(s_empty + x));
+        }
+        const float4 *nl4 = reinterpret_cast<const float4 *>(col_nl + x * 128 + q * 32);
+        const int4 *ip4 = reinterpret_cast<const int4 *>(col_ip + x * 128 + q * 32);
+        if constexpr (MOD == 2) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], c);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = ex2(v[e]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) add2(v[e], v[e + 1], 1.f, 1.f);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = rcp_approx(v[e]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 n = nl4[e >> 2];
+            fma2v(v[e], v[e + 1], -2.f * p.softcap_log2, n.x + p.softcap_log2, n.y + p.softcap_log2);
+            fma2v(v[e + 2], v[e + 3], -2.f * p.softcap_log2, n.z + p.softcap_log2, n.w + p.softcap_log2);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 n = nl4[e >> 2];
+            if constexpr (MOD == 1) {
+              const int4 i = ip4[e >> 2];
+              n.x = fmaf(-p.alibi_log2, fabsf((float)(i.x - j)), n.x);
+              n.y = fmaf(-p.alibi_log2, fabsf((float)(i.y - j)), n.y);
+              n.z = fmaf(-p.alibi_log2, fabsf((float)(i.z - j)), n.z);
+              n.w = fmaf(-p.alibi_log2, fabsf((float)(i.w - j)), n.w);
+            }
+            fma2v(v[e], v[e + 1], c, n.x, n.y);
+            fma2v(v[e + 2], v[e + 3], c, n.z, n.w);
+          }
+        }
+        if (mask) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const int4 i = ip4[e >> 2];
+            const int ii[4] = {i.x, i.y, i.z, i.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              bool vis = ii[k] > INT_MIN / 4;
+              if (p.causal) vis = vis && j <= ii[k];
+              if (p.window > 0) vis = vis && (p.causal ? ii[k] - j < p.window : abs(ii[k] - j) < p.window);
+              v[e + k] = vis ? v[e + k] : -INFINITY;
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          add2(acc[0], acc[1], ex2(v[e]), ex2(v[e + 1]));
+          add2(acc[2], acc[3], ex2(v[e + 2]), ex2(v[e + 3]));
+        }
+      }
+      total += (acc[0] + acc[1]) + (acc[2] + acc[3]);   // a tile's sum first: shorter chains of roundings
+    }
+    if (ok && j0_64 + r < p.extent) {
+      const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
+      float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
+      const float gain = j < s.sk ? total : 0.f;
+      if (!p.inplace || j < s.sk) wo[j] = wi ? fmaf(p.beta, wi[j], gain) : gain;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -1,0 +1,114 @@
+// Instantiations and launcher of the shared-prefix pass (fa_prefix.cuh), and
+// the merge of its partials with those of the sequences' own keys.
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+template <int D, int KV, int MOD>
+cudaError_t prefix_one(const PrefixLaunch &L) {
+  using Cfg = PrefixCfg<D, KV>;
+  static unsigned long long done = 0;
+  auto kern = fa_prefix_kernel<D, KV, MOD>;
+  cudaError_t e = ensure_smem_attr(kern, Cfg::kSmemBytes, &done);
+  if (e != cudaSuccess) return e;
+  kern<<<L.grid, Cfg::kThreads, Cfg::kSmemBytes, L.stream>>>(L.tm_q, L.tm_k, L.tm_v, L.p);
+  return cudaGetLastError();
+}
+
+template <int D, int KV>
+cudaError_t prefix_mod(const PrefixLaunch &L) {
+  if (L.mod == 1) return prefix_one<D, KV, 1>(L);
+  if (L.mod == 2) return prefix_one<D, KV, 2>(L);
+  return prefix_one<D, KV, 0>(L);
+}
+
+template <int D>
+cudaError_t prefix_kv(const PrefixLaunch &L) {
+  if (L.kv == 1) return prefix_mod<D, 1>(L);
+  if (L.kv == 2) return prefix_mod<D, 2>(L);
+  return prefix_mod<D, 0>(L);
+}
+
+// LSE = ln sum_s exp(LSE_s), out = sum_s exp(LSE_s - LSE) O_s.  One warp per
+// (row, head): the partial LSEs are read by the lanes at once, and the partial
+// rows in batches of four so that their latencies overlap.  A partial with
+// LSE -inf was not written and is not read.
+template <int D>
+__global__ void __launch_bounds__(128) fa_prefix_merge_kernel(const float *__restrict__ o_part,
+                                                              const float *__restrict__ lse_part,
+                                                              const int32_t *__restrict__ cu_q, int num_seqs,
+                                                              int num_splits, int64_t n_rows, int hq,
+                                                              __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+  const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (wid >= n_rows * hq) return;
+  const int64_t t = wid / hq;
+  const int h = (int)(wid % hq);
+  if (t >= __ldg(cu_q + num_seqs)) return;   // rows behind the last sequence stay as they were
+  constexpr int kPer = D / 32;
+  float acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  float m = -INFINITY, den = 0.f;
+  // 32 partials at a time, with a running maximum
+  for (int s0 = 0; s0 < num_splits; s0 += 32) {
+    const float ls = s0 + lane < num_splits ? lse_part[((int64_t)(s0 + lane) * hq + h) * n_rows + t] : -INFINITY;
+    float mx = ls;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (mx == -INFINITY) continue;
+    const float mn = fmaxf(m, mx), a = ex2((m - mn) * kLog2e);
+    m = mn;
+    const float w = ex2((ls - mn) * kLog2e);
+    float ws = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    den = den * a + ws;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= a;
+    const int cnt = min(32, num_splits - s0);
+    for (int s = 0; s < cnt; s += 4) {
+      float v[4][kPer], ww[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        ww[u] = __shfl_sync(0xffffffffu, w, (s + u) & 31);
+        const bool on = s + u < cnt && __shfl_sync(0xffffffffu, ls, (s + u) & 31) != -INFINITY;
+        if (!on) ww[u] = 0.f;
+        const float *src = o_part + (((int64_t)(s0 + s + u) * n_rows + t) * hq + h) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 x = on ? *reinterpret_cast<const float2 *>(src + e) : make_float2(0.f, 0.f);
+          v[u][e] = x.x;
+          v[u][e + 1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(ww[u], v[u][e], acc[e]);
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  __nv_bfloat16 *dst = out + (t * hq + h) * D + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lse && lane == 0) lse[(int64_t)h * n_rows + t] = den > 0.f ? m + __log2f(den) * kLn2 : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(int d, const PrefixLaunch &L) { return d == 64 ? prefix_kv<64>(L) : prefix_kv<128>(L); }
+
+cudaError_t launch_prefix_merge(int d, const float *o_part, const float *lse_part, const int32_t *cu_q, int num_seqs,
+                                int num_splits, int64_t n_rows, int hq, void *out, float *lse, cudaStream_t stream) {
+  const int threads = 128;
+  const unsigned blocks = (unsigned)((n_rows * hq * 32 + threads - 1) / threads);
+  auto *o = reinterpret_cast<__nv_bfloat16 *>(out);
+  auto kern = d == 64 ? fa_prefix_merge_kernel<64> : fa_prefix_merge_kernel<128>;
+  kern<<<blocks, threads, 0, stream>>>(o_part, lse_part, cu_q, num_seqs, num_splits, n_rows, hq, o, lse);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -1,0 +1,710 @@
+// fa_prefix.cuh -- the shared part of a decode batch whose sequences begin
+// with the same pages: one attention pass over the prefix keys of a group of
+// sequences for all query rows of the group at once.
+//
+// Decode reads the cache once per sequence.  Where the sequences of a group
+// hold the same first pages, those keys can be read once per group instead:
+// the rows (query token, head of the kv head's group) of all its sequences are
+// one matrix Q [tokens * Hq/Hkv, D], and the prefix part of the attention is
+// the dense product of the prefill -- O = softmax(Q K^T) V, with the running
+// maximum and sum -- whose partial (O, LSE) merges with the partials of each
+// sequence's own keys by the split-KV rule
+//   LSE = ln sum_s exp(LSE_s),  out = sum_s exp(LSE_s - LSE) O_s.
+//
+// CTA (key split, kv head, tile of 128 rows): S = Q K^T and O += P V on tcgen05
+// with S, P and O in TMEM.  A TMA box of {64 columns, Hq/Hkv heads, 128 /
+// (Hq/Hkv) tokens} lands Q with the heads of a kv head beside each other, so a
+// GQA group fills the tile's rows and K/V are read once for all its heads.  One
+// tile per CTA and two CTAs per SM: one CTA's softmax runs under the other's
+// products, and 64 KB of K and V are in flight per CTA.
+//
+// Every row has its own interval of visible keys (its sequence's length,
+// causal limit and window), so the result does not depend on the prefix lying
+// left of all queries; key tiles that no row sees are not loaded.
+//
+// Byte caches (KV 1 e4m3, 2 int8): two converter warps turn the staged bytes
+// into f16 (exact) in place; k_scale multiplies the scores and v_scale the
+// weights in fp32.  The reference of the exponentials includes the tile's
+// largest v_scale, so that the scaled weights use f16's range whatever the
+// magnitude of V.
+#pragma once
+#include <climits>
+
+#include "fa_decode.cuh"
+#include "fa_prefill.cuh"
+
+namespace fa {
+
+struct PrefixParams {
+  const int32_t *cu_q, *cu_k;
+  const int32_t *cu_groups;      // [num_groups + 1]: sequences of a group
+  const int32_t *prefix_lens;    // [num_groups]
+  int32_t num_groups, num_seqs;
+  const int32_t *block_table;
+  int64_t bt_stride, max_pages, n_pages;
+  int32_t page_size, page_shift, rows_per_box;
+  int32_t gather;
+  KvGather gk, gv;
+  const float *k_scale, *v_scale;
+  int64_t total_q;
+  int32_t hq, hkv, group, tokens_per_tile;
+  int32_t num_splits;
+  float *o_part;                 // [splits of the whole call][T_q][Hq][D]; this pass writes the first num_splits
+  float *lse_part;               // [splits of the whole call][Hq][T_q]
+  int32_t causal, window;
+  float scale_log2, alibi_log2, softcap_arg, softcap_log2;
+  int *err;
+};
+
+template <int D, int KV>
+struct PrefixCfg {
+  static constexpr int KC = D / 64;
+  static constexpr int kChunkBytes = 128 * 128;        // one 64-column block of 128 rows, 16-bit
+  static constexpr int kTileBytes = KC * kChunkBytes;
+  static constexpr int NS = D == 64 ? 2 : 1;           // K and V stages
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kTileBytes;
+  static constexpr int kOffV = kOffK + NS * kTileBytes;
+  // byte caches: scales of NSS tiles, [128 of K, 128 of V] each.  Tile j's take
+  // the slot of tile j - NS - 1: its K bytes landed after QK(j - NS), which was
+  // issued after the softmax of tile j - NS - 1.
+  static constexpr int NSS = NS + 1;
+  static constexpr int kOffSc = kOffV + NS * kTileBytes;
+  static constexpr int kOffBar = kOffSc + (KV ? NSS * 256 * 4 : 0);
+  static constexpr int kNumBars = 2 + 6 * NS + 3 + NSS;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+  static constexpr int kThreads = 8 * 32;
+  static constexpr uint32_t kTmemCols = 256;           // S (and P) [0,128), O [128, 128 + D)
+  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+};
+
+// Bounded wait that does not give up on the abort flag: for copies in flight
+// when a CTA ends.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitCycles) {
+  }
+}
+
+__device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 32 bytes, one sector.
+__device__ __forceinline__ void st_global_f8(float *dst, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// MOD: 0 plain with a positive scale, 1 ALiBi (or any scale), 2 soft-cap.
+template <int D, int KV, int MOD>
+__global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
+    fa_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
+  using Cfg = PrefixCfg<D, KV>;
+  constexpr int KC = Cfg::KC, NS = Cfg::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x, hk = blockIdx.y;
+
+  // ------------------------------------------------------------ work tile --
+  // The tiles of all groups in a row; every warp finds this one's group.
+  int grp = -1, tile = 0, q0 = 0, nq = 0;   // group, tile within it, its first token and token count
+  {
+    int before = 0;
+    for (int g0 = 0; g0 < p.num_groups && grp < 0; g0 += 32) {
+      const int g = g0 + lane;
+      int first = 0, cnt = 0;
+      if (g < p.num_groups) {
+        const int s0 = min(max(__ldg(p.cu_groups + g), 0), p.num_seqs);
+        const int s1 = min(max(__ldg(p.cu_groups + g + 1), s0), p.num_seqs);
+        first = __ldg(p.cu_q + s0);
+        cnt = __ldg(p.cu_q + s1) - first;
+      }
+      int tiles = cnt > 0 ? (cnt + p.tokens_per_tile - 1) / p.tokens_per_tile : 0;
+      int incl = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + incl > (int)blockIdx.z);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        grp = g0 + l;
+        tile = (int)blockIdx.z - before - __shfl_sync(0xffffffffu, incl - tiles, l);
+        q0 = __shfl_sync(0xffffffffu, first, l);
+        nq = __shfl_sync(0xffffffffu, cnt, l);
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  if (split == 0 && hk == 0 && blockIdx.z == 0 && threadIdx.x == 0 &&
+      (__ldg(p.cu_groups) != 0 || __ldg(p.cu_groups + p.num_groups) != p.num_seqs))
+    record_error(p.err, kErrBounds);   // some sequence is in no group
+  if (grp < 0) return;
+  const int s0 = min(max(__ldg(p.cu_groups + grp), 0), p.num_seqs);
+  const int s1 = min(max(__ldg(p.cu_groups + grp + 1), s0), p.num_seqs);
+  const int tok0 = q0 + tile * p.tokens_per_tile;
+  const int rows = min(p.tokens_per_tile, q0 + nq - tok0) * p.group;
+  const int plen = prefix_keys(p.prefix_lens, grp, p.page_size, p.max_pages);
+
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
+  uint64_t *q_full = bars, *q_conv = bars + 1, *k_full = bars + 2, *k_empty = k_full + NS, *k_stage = k_empty + NS,
+           *v_full = k_stage + NS, *v_empty = v_full + NS, *v_stage = v_empty + NS, *s_full = v_stage + NS,
+           *p_full = s_full + 1, *o_done = p_full + 1, *sc_full = o_done + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::kOffMisc + 8);
+  int *range = reinterpret_cast<int *>(smem + Cfg::kOffMisc + 16);   // keys that any row sees
+  if (threadIdx.x == 0) {
+    range[0] = INT_MAX;
+    range[1] = 0;
+    *abort_flag = 0;
+    const uint32_t n_fill = p.gather ? 32u : 1u;
+    mbar_init(smem_u32(q_full), 1);
+    mbar_init(smem_u32(q_conv), 128);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(k_full + i), KV ? 4 * KC : n_fill);
+      mbar_init(smem_u32(k_empty + i), 1);
+      mbar_init(smem_u32(k_stage + i), n_fill);
+      mbar_init(smem_u32(v_full + i), KV ? 4 * KC : n_fill);
+      mbar_init(smem_u32(v_empty + i), 1);
+      mbar_init(smem_u32(v_stage + i), n_fill);
+    }
+    mbar_init(smem_u32(s_full), 1);
+    mbar_init(smem_u32(p_full), 128);
+    mbar_init(smem_u32(o_done), 1);
+    for (int i = 0; i < Cfg::NSS; ++i) mbar_init(smem_u32(sc_full + i), 2);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  // Row r < rows: token tok0 + r / group, head hk * group + r % group, and the
+  // keys [row_lo, row_hi) of the prefix it sees.  Rows past the last see
+  // everything (they are never stored and must force no masking).
+  int row_lo = 0, row_hi = INT_MAX, ip = 0;
+  if (threadIdx.x < 128) {
+    const int r = threadIdx.x;
+    if (r < rows) {
+      const int tok = tok0 + r / p.group;
+      const int b = upper_bound_i32(p.cu_q, s0, s1, tok) - 1;
+      const int qa = __ldg(p.cu_q + b), sq = __ldg(p.cu_q + b + 1) - qa;
+      const int sk = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+      ip = tok - qa + sk - sq;
+      row_hi = min(plen, sk);
+      if (p.causal) row_hi = min(row_hi, ip + 1);
+      if (p.window > 0) {
+        row_lo = max(0, ip - p.window + 1);
+        if (!p.causal) row_hi = min(row_hi, ip + p.window);
+      }
+      if (row_hi <= row_lo) row_lo = row_hi = 0;
+    }
+    int lo = (r < rows && row_hi > row_lo) ? row_lo : INT_MAX, hi = (r < rows) ? row_hi : 0;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicMin(range, lo);
+      atomicMax(range + 1, hi);
+    }
+  }
+  __syncthreads();
+  // this split's key tiles, of those that some row sees
+  int kt_lo, kt_hi;
+  {
+    const int a = range[1] > 0 ? range[0] / kBlockN : 0, e = (range[1] + kBlockN - 1) / kBlockN;
+    const int per = e > a ? (e - a + p.num_splits - 1) / p.num_splits : 0;
+    kt_lo = a + split * per;
+    kt_hi = min(e, kt_lo + per);
+  }
+  if (kt_hi <= kt_lo) {
+    for (int r = threadIdx.x; r < rows; r += Cfg::kThreads)
+      p.lse_part[((int64_t)split * p.hq + hk * p.group + r % p.group) * p.total_q + tok0 + r / p.group] = -INFINITY;
+    return;
+  }
+  const int n_tiles = kt_hi - kt_lo;
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint8_t *sQ = smem + Cfg::kOffQ, *sK = smem + Cfg::kOffK, *sV = smem + Cfg::kOffV;
+  float *sSc = reinterpret_cast<float *>(smem + Cfg::kOffSc);
+  const int32_t *bt = p.block_table + (int64_t)s0 * p.bt_stride;   // the group's first sequence
+  // page of prefix key `key`; -1 past the prefix (zero rows) or outside the pool (flagged)
+  auto page_of = [&](int key) -> int {
+    if (key >= plen) return -1;
+    const int pg = __ldg(bt + (key >> p.page_shift));
+    if (pg < 0 || pg >= p.n_pages) {
+      record_error(p.err, kErrBounds);
+      return -1;
+    }
+    return pg;
+  };
+
+  if (warp == 4) {
+    // ------------------------------------------------ producer: Q, K, V --
+    if (lane == 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      mbar_expect_tx(smem_u32(q_full), (uint32_t)(KC * p.tokens_per_tile * p.group * 128));
+      for (int c = 0; c < KC; ++c)
+        tma_load_3d(smem_u32(sQ + c * Cfg::kChunkBytes), &tm_q, smem_u32(q_full), c * 64, hk * p.group, tok0);
+    }
+    uint64_t *kb = KV ? k_stage : k_full, *vb = KV ? v_stage : v_full;
+    bool ok = true;
+    int j = 0;
+    if (p.gather) {
+      GatherPipe<1> gp;
+      // One slot in flight.  Waiting to refill K's slot the newest is V(j-1):
+      // QK(j-NS), which frees the slot, needs K up to j-NS and V up to
+      // j-NS-1.  Waiting for V's slot the newest is K(j): PV(j-NS) needs K and
+      // V up to j-NS.
+      auto pages = [&](int kt, int (&pg)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pg[u] = kt < kt_hi ? page_of(kt * kBlockN + lane + 32 * u) : -1;
+      };
+      int pg[4], pgn[4];
+      pages(kt_lo, pg);
+      for (; ok && j < n_tiles; ++j) {
+        const int st = j % NS, key0 = (kt_lo + j) * kBlockN;
+        pages(kt_lo + j + 1, pgn);
+        if (lane == 0 && j >= NS) ok = mbar_wait(smem_u32(k_empty + st), ((j / NS) - 1) & 1, abort_flag, p.err);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          uint8_t *dst = sK + st * Cfg::kTileBytes + c * Cfg::kChunkBytes;
+          if constexpr (KV) gather_block<kBlockN, 64, kGatherStage>(dst, p.gk, hk, key0, p.page_size - 1, c * 64, pg, lane);
+          else gather_block<kBlockN, 128, kGatherSw128>(dst, p.gk, hk, key0, p.page_size - 1, c * 128, pg, lane);
+        }
+        gp.commit(smem_u32(kb + st));
+        if (lane == 0 && j >= NS) ok = mbar_wait(smem_u32(v_empty + st), ((j / NS) - 1) & 1, abort_flag, p.err);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          uint8_t *dst = sV + st * Cfg::kTileBytes + c * Cfg::kChunkBytes;
+          if constexpr (KV) gather_block<kBlockN, 64, kGatherStage>(dst, p.gv, hk, key0, p.page_size - 1, c * 64, pg, lane);
+          else gather_block<kBlockN, 128, kGatherSw128>(dst, p.gv, hk, key0, p.page_size - 1, c * 128, pg, lane);
+        }
+        gp.commit(smem_u32(vb + st));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pg[u] = pgn[u];
+      }
+      gp.drain();
+    } else {
+      // Lane l < 128 / rows_per_box lands the boxes of rows l * rows_per_box..;
+      // page ids are read one tile ahead.
+      const int rb = p.rows_per_box, r0 = lane * rb;
+      const bool boxer = r0 < kBlockN;
+      auto page_at = [&](int kt) { return (boxer && kt < kt_hi) ? page_of(kt * kBlockN + r0) : -1; };
+      constexpr uint32_t kBytes = KV ? 128u * D : (uint32_t)Cfg::kTileBytes;
+      auto load = [&](const CUtensorMap *tm, uint8_t *dst, uint64_t *bar, int kt, int pg) {
+        if (!boxer) return;
+        const int slot = (kt * kBlockN + r0) & (p.page_size - 1);
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          uint8_t *at = dst + c * Cfg::kChunkBytes;
+          // bytes: raw rows of 64 in the upper half of their 32-row slice
+          at += KV ? (r0 >> 5) * 4096 + 2048 + (r0 & 31) * 64 : r0 * 128;
+          tma_load_4d(smem_u32(at), tm, smem_u32(bar), c * 64, hk, slot, pg);
+        }
+      };
+      int pg = page_at(kt_lo);
+      for (; ok && j < n_tiles; ++j) {
+        const int st = j % NS, kt = kt_lo + j;
+        const int pg_next = page_at(kt + 1);
+        if (lane == 0) {
+          if (j >= NS) ok = mbar_wait(smem_u32(k_empty + st), ((j / NS) - 1) & 1, abort_flag, p.err);
+          if (ok) mbar_expect_tx(smem_u32(kb + st), kBytes);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        load(&tm_k, sK + st * Cfg::kTileBytes, kb + st, kt, pg);
+        if (lane == 0) {
+          if (j >= NS) ok = mbar_wait(smem_u32(v_empty + st), ((j / NS) - 1) & 1, abort_flag, p.err);
+          if (ok) mbar_expect_tx(smem_u32(vb + st), kBytes);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+          if (lane == 0) mbar_drain(smem_u32(kb + st), (j / NS) & 1);
+          break;
+        }
+        load(&tm_v, sV + st * Cfg::kTileBytes, vb + st, kt, pg);
+        pg = pg_next;
+      }
+      // copies in flight land before the CTA ends, whatever the others do
+      if (lane == 0)
+        for (int i = max(0, j - NS); i < j; ++i) {
+          mbar_drain(smem_u32(kb + i % NS), (i / NS) & 1);
+          mbar_drain(smem_u32(vb + i % NS), (i / NS) & 1);
+        }
+    }
+    if (lane == 0) mbar_drain(smem_u32(q_full), 0);
+  } else if (warp == 5) {
+    // ------------------------------------------------------- MMA issuer --
+    if (lane == 0) {
+      constexpr uint32_t id_qk = KV ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+      constexpr uint32_t id_pv = KV ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(sV), 128 * 128, 1024);
+      const uint32_t hi = (uint32_t)(dq >> 32), lo_q = (uint32_t)dq;
+      const uint32_t lo_k = (uint32_t)smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint32_t lo_v = (uint32_t)dv, hi_v = (uint32_t)(dv >> 32);
+      auto qk = [&](int st) {
+        uint32_t a = lo_q, b = lo_k + (uint32_t)(st * (Cfg::kTileBytes >> 4));
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          if (ks == 0) mma_ss_w<0>(tmem, a, hi, b, hi, id_qk);
+          else mma_ss_w<1>(tmem, a, hi, b, hi, id_qk);
+          const uint32_t step = ((ks + 1) & 3) ? 2u : (uint32_t)((128 * 128 - 96) >> 4);
+          a += step;
+          b += step;
+        }
+        tc_commit(smem_u32(s_full));
+        tc_commit(smem_u32(k_empty + st));
+      };
+      bool ok = mbar_wait(smem_u32(KV ? q_conv : q_full), 0, abort_flag, p.err);
+      if (ok) ok = mbar_wait(smem_u32(k_full), 0, abort_flag, p.err);
+      if (ok) {
+        tc_fence_after();
+        qk(0);
+      }
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int st = j % NS, sn = (j + 1) % NS;
+        if (!(ok = mbar_wait(smem_u32(v_full + st), (j / NS) & 1, abort_flag, p.err))) break;
+        if (!(ok = mbar_wait(smem_u32(p_full), j & 1, abort_flag, p.err))) break;
+        tc_fence_after();
+        uint32_t b = lo_v + (uint32_t)(st * (Cfg::kTileBytes >> 4));
+#pragma unroll
+        for (int ks = 0; ks < kBlockN / 16; ++ks) {
+          mma_ts_w(tmem + 128, tmem + ks * 8, b, hi_v, id_pv, (ks > 0 || j > 0) ? 1u : 0u);
+          b += (16 * 128) >> 4;
+        }
+        tc_commit(smem_u32(o_done));
+        tc_commit(smem_u32(v_empty + st));
+        if (j + 1 < n_tiles) {
+          if (!(ok = mbar_wait(smem_u32(k_full + sn), ((j + 1) / NS) & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          qk(sn);
+        }
+      }
+    }
+  } else if (warp >= 6) {
+    // ---------------------------------------- converters (byte caches) --
+    // Slices of 32 rows x 64 columns, K's then V's of a tile, alternate
+    // between the two warps.  A slice's bytes lie in the upper half of its own
+    // f16 output: step t writes rows 8t..8t+7, whose 1 KB overlaps only
+    // staging rows that earlier steps (or this step, before its writes) read.
+    if constexpr (KV != 0) {
+      const int cw = warp - 6;
+      // warp 6 brings the K scales of a tile, warp 7 the V scales, one tile ahead
+      const float *sc_src = cw ? p.v_scale : p.k_scale;
+      auto scales = [&](int kt, float (&s)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          s[u] = 0.f;
+          if (kt >= kt_hi) continue;
+          const int key = kt * kBlockN + lane + 32 * u;
+          const int pg = page_of(key);
+          if (pg >= 0) s[u] = __ldg(sc_src + ((int64_t)pg * p.page_size + (key & (p.page_size - 1))) * p.hkv + hk);
+        }
+      };
+      float sc[4], scn[4];
+      scales(kt_lo, sc);
+      bool ok = true;
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int st = j % NS;
+        scales(kt_lo + j + 1, scn);
+        for (int half = 0; ok && half < 2; ++half) {
+          uint64_t *stage = half ? v_stage : k_stage, *full = half ? v_full : k_full;
+          ok = mbar_wait(smem_u32(stage + st), (j / NS) & 1, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t *tile_base = (half ? sV : sK) + st * Cfg::kTileBytes;
+          for (int sl = cw; sl < 4 * KC; sl += 2) {
+            uint8_t *base = tile_base + (sl >> 2) * Cfg::kChunkBytes + (sl & 3) * 4096;
+            const uint8_t *stg = base + 2048;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int rr = 8 * t + (lane >> 2), part = lane & 3;
+              const uint4 raw = *reinterpret_cast<const uint4 *>(stg + rr * 64 + part * 16);
+              uint32_t h[8];
+              dec_bytes4_to_f16<KV>(raw.x, h[0], h[1]);
+              dec_bytes4_to_f16<KV>(raw.y, h[2], h[3]);
+              dec_bytes4_to_f16<KV>(raw.z, h[4], h[5]);
+              dec_bytes4_to_f16<KV>(raw.w, h[6], h[7]);
+              __syncwarp();   // every lane has read this step's rows
+              *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(full + st));
+          }
+          if (half == 0) {
+            float *dst = sSc + (j % Cfg::NSS) * 256 + cw * 128;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dst[lane + 32 * u] = sc[u];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sc_full + j % Cfg::NSS));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sc[u] = scn[u];
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- softmax --
+    const int r = threadIdx.x;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const uint32_t sa = tmem + lane_base, oa = tmem + lane_base + 128;
+    bool ok = true;
+    float rowf = 1.f;
+    if constexpr (KV != 0) {
+      // Q to f16 in place, with a power-of-two factor per row (max|q| 2^e in
+      // [2^14, 2^15)); row r owns 128 bytes of each block, visited from chunk
+      // r mod 8 on so that a warp's accesses spread over all banks.
+      ok = mbar_wait(smem_u32(q_full), 0, abort_flag, p.err);
+      if (ok) {
+        uint8_t *qrow = sQ + r * 128;
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(qrow + c * Cfg::kChunkBytes + ((u + r) & 7) * 16);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(ww[k] << 16)), fabsf(__uint_as_float(ww[k] & 0xFFFF0000u))));
+          }
+        int sh = 0;
+        if (amax > 0.f && amax <= 3.0e38f) sh = min(141 - (int)((__float_as_uint(amax) >> 23) & 0xFF), 126);
+        const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
+        rowf = __uint_as_float((uint32_t)(127 - sh) << 23);
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint4 *ptr = reinterpret_cast<uint4 *>(qrow + c * Cfg::kChunkBytes + ((u + r) & 7) * 16);
+            const uint4 w = *ptr;
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t hh[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              hh[k] = pack_f16x2(__uint_as_float(ww[k] << 16) * up, __uint_as_float(ww[k] & 0xFFFF0000u) * up);
+            *ptr = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+          }
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(smem_u32(q_conv));
+    }
+    const float sl2 = p.scale_log2 * rowf;
+    const float c2u = 2.f * kLog2e * p.softcap_arg * rowf;
+    // plain bf16 scores stay raw, the scale rides in the exponent's FMA
+    constexpr bool raw = MOD == 0 && KV == 0;
+    const float cexp = raw ? sl2 : 1.f;
+    float m_ref = -INFINITY, l = 0.f;
+    for (int j = 0; ok && j < n_tiles; ++j) {
+      const int j0 = (kt_lo + j) * kBlockN;
+      const float *ks = sSc + (j % Cfg::NSS) * 256, *vs = ks + 128;
+      float lv = 0.f;      // log2 of the tile's largest v_scale (held above 2^-40, see below)
+      if constexpr (KV != 0) {
+        ok = mbar_wait(smem_u32(sc_full + j % Cfg::NSS), (j / Cfg::NSS) & 1, abort_flag, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const float4 v4 = *reinterpret_cast<const float4 *>(vs + 4 * lane);
+        float mv = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        // exp2(s - m) of the row sum is then at most 2^40 above its usual range
+        lv = __log2f(fminf(fmaxf(mv, 0x1p-40f), 0x1p40f));
+      }
+      const bool need_mask = __any_sync(0xffffffffu, j0 < row_lo || j0 + kBlockN > row_hi);
+      ok = mbar_wait(smem_u32(s_full), j & 1, abort_flag, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float alpha_tile = 1.f;
+      bool warp_need = false;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float v[64];
+        tmem_ld32(sa + hf * 64, *reinterpret_cast<float(*)[32]>(v));
+        tmem_ld32(sa + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+        tmem_wait_ld();
+        const int jc = j0 + hf * 64;
+        if constexpr (!raw) {
+          const float f = MOD == 2 ? c2u : sl2;
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            if constexpr (KV != 0) {
+              const float4 k4 = *reinterpret_cast<const float4 *>(ks + hf * 64 + e);
+              v[e] *= k4.x * f;
+              v[e + 1] *= k4.y * f;
+              v[e + 2] *= k4.z * f;
+              v[e + 3] *= k4.w * f;
+            } else {
+              mul2(v[e], v[e + 1], f);
+              mul2(v[e + 2], v[e + 3], f);
+            }
+          }
+          if constexpr (MOD == 2) {
+            const float cl = p.softcap_log2;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) v[e] = ex2(v[e]);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) add2(v[e], v[e + 1], 1.f, 1.f);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) v[e] = rcp_approx(v[e]);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) fma2(v[e], v[e + 1], v[e], v[e + 1], -2.f * cl, cl);
+          }
+          if constexpr (MOD == 1) {
+            const float dbase = (float)(ip - jc);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) v[e] = fmaf(-p.alibi_log2, fabsf(dbase - (float)e), v[e]);
+          }
+        }
+        if (need_mask) {
+          const int elo = row_lo - jc, ehi = row_hi - jc;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e] = (e >= elo && e < ehi) ? v[e] : -INFINITY;
+        }
+        float t1[22];
+#pragma unroll
+        for (int k = 0; k < 21; ++k) t1[k] = max3(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
+        t1[21] = v[63];
+        float t2[8];
+#pragma unroll
+        for (int k = 0; k < 7; ++k) t2[k] = max3(t1[3 * k], t1[3 * k + 1], t1[3 * k + 2]);
+        t2[7] = t1[21];
+        float hmax = fmaxf(max3(t2[0], t2[1], t2[2]), fmaxf(max3(t2[3], t2[4], t2[5]), fmaxf(t2[6], t2[7])));
+        if (raw && hmax != -INFINITY) hmax *= sl2;
+        if constexpr (KV != 0) hmax += lv;
+        const float m_new = fmaxf(m_ref, hmax);
+        const bool need = m_new > m_ref + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2(m_ref - m_new) : 1.f;   // 0 when m_ref is -inf
+          if (need) {
+            m_ref = m_new;
+            l *= alpha;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[q] *= alpha;
+          }
+          alpha_tile *= alpha;
+          warp_need = true;
+          if (hf == 1) {
+            // P of the first half was taken against the old reference
+            tmem_wait_st();
+            float pw[32];
+            tmem_ld32(sa, pw);
+            tmem_wait_ld();
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t u = __float_as_uint(pw[e]);
+              if constexpr (KV != 0) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                w[e] = pack_f16x2(f.x * alpha, f.y * alpha);
+              } else {
+                w[e] = pack_bf16x2(__uint_as_float(u << 16) * alpha, __uint_as_float(u & 0xFFFF0000u) * alpha);
+              }
+            }
+            tmem_st32(sa, w);
+          }
+        }
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float t0, t1_, t2_, t3;
+            fma2(t0, t1_, v[32 * c + e], v[32 * c + e + 1], cexp, -m_use);
+            fma2(t2_, t3, v[32 * c + e + 2], v[32 * c + e + 3], cexp, -m_use);
+            t0 = ex2(t0);
+            t1_ = ex2(t1_);
+            t2_ = ex2(t2_);
+            t3 = ex2(t3);
+            add2(sum[0], sum[1], t0, t1_);
+            add2(sum[2], sum[3], t2_, t3);
+            if constexpr (KV != 0) {
+              const float4 v4 = *reinterpret_cast<const float4 *>(vs + hf * 64 + 32 * c + e);
+              pk[e / 2] = pack_f16x2(t0 * v4.x, t1_ * v4.y);
+              pk[e / 2 + 1] = pack_f16x2(t2_ * v4.z, t3 * v4.w);
+            } else {
+              pk[e / 2] = pack_bf16x2(t0, t1_);
+              pk[e / 2 + 1] = pack_bf16x2(t2_, t3);
+            }
+          }
+          prefix_tmem_st16(sa + hf * 32 + c * 16, pk);
+        }
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (warp_need && j > 0) {
+        ok = mbar_wait(smem_u32(o_done), (j - 1) & 1, abort_flag, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(oa + c * 32, o);
+          tmem_wait_ld();
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * alpha_tile);
+          tmem_st32(oa + c * 32, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(p_full));
+    }
+    // -------------------------------------------------------- epilogue --
+    if (ok) {
+      ok = mbar_wait(smem_u32(o_done), (n_tiles - 1) & 1, abort_flag, p.err);
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        const bool has = l > 0.f;
+        const float inv = has ? 1.f / l : 0.f;
+        const int64_t t = (int64_t)tok0 + r / p.group;
+        const int h = hk * p.group + r % p.group;
+        float *dst = p.o_part + (((int64_t)split * p.total_q + t) * p.hq + h) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(oa + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = has ? o[e] * inv : 0.f;
+          if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) st_global_f8(dst + c * 32 + e, o + e);
+          }
+        }
+        if (r < rows)
+          p.lse_part[((int64_t)split * p.hq + h) * p.total_q + t] = has ? (m_ref + __log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmemCols);
+  }
+}
+
+}  // namespace fa

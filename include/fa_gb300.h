@@ -1,9 +1,10 @@
 /*
  * fa_gb300.h -- C ABI of the GB300 (sm_103a) attention forward library.
  *
- * One operation, in several entry points: the FlashAttention forward pass
- * over packed variable-length sequences and a paged KV cache, with per-row
- * log-sum-exp output.  For query row i of sequence b and head h:
+ * The FlashAttention forward pass over packed variable-length sequences and a
+ * paged KV cache, with per-row log-sum-exp output, its backward pass, and the
+ * operators of a serving loop around the paged decode (shared prefixes, key
+ * weights, eviction).  The forward:  For query row i of sequence b and head h:
  *
  *   out[i]  = sum_j softmax_j(s_ij) * v_j        over the keys j the mask allows
  *   lse[i]  = log sum_j exp(s_ij)                (natural log)
@@ -381,6 +382,172 @@ FA_API fa_status_t fa_fwd_varlen_noalloc(const fa_tensor_t *q, const fa_tensor_t
                                   int32_t causal, int32_t window, const fa_score_mod_t *score_mod,
                                   const fa_block_mask_t *block_mask, const fa_prologue_t *prologue,
                                   int32_t page_size, const fa_launch_t *launch, void *stream);
+
+/*
+ * Decode of a batch whose sequences share prefixes.
+ *
+ * fa_fwd_shared_prefix computes what fa_fwd_varlen computes -- same arguments,
+ * layouts, masks and results -- for a paged batch of few query rows per
+ * sequence, and reads the keys that a group of sequences shares once for the
+ * whole group instead of once per sequence.
+ *
+ * The sequences come in groups, in order: group g holds the sequences
+ * cu_groups[g] ... cu_groups[g + 1] - 1 (cu_groups[0] = 0 and
+ * cu_groups[num_groups] = num_seqs; a violation records
+ * FA_ERR_DEVICE_BOUNDS and the rows left out are undefined).  The sequences of
+ * group g hold the same keys first: lens[g] of them, rounded down to whole
+ * pages, in the same pages.  Their block-table rows repeat those pages; the
+ * group's first row is read.  Lengths (cu_seqlens_k) count the shared keys.
+ * Each row keeps its own causal limit, window and length, also inside the
+ * prefix, and a group of one sequence or a prefix of 0 keys is fine.
+ *
+ * max_len and num_splits only size the work: max_len bounds lens[] (a longer
+ * prefix is still attended in full), num_splits >= 1 cuts each prefix into
+ * that many key ranges (fa_shared_prefix_default_splits).  launch->num_splits
+ * >= 1 cuts the keys behind the prefix likewise, sized by max_seqlen_k -
+ * max_len.
+ */
+typedef struct {
+    const int32_t *cu_groups;   /* device, int32 [num_groups + 1] */
+    const int32_t *lens;        /* device, int32 [num_groups] */
+    int32_t num_groups;
+    int32_t max_len;
+    int32_t num_splits;
+} fa_shared_prefix_t;
+
+/*
+ *  q, out, lse   as fa_fwd_varlen; q bf16, Dk = Dv in {64, 128},
+ *                max_seqlen_q * Hq/Hkv <= 16.
+ *  k_cache, v_cache, k_scale, v_scale, block_table, page_size
+ *                token-major pages [N_pg, P_s, Hkv, D] of 1 ... 1024 keys,
+ *                bf16, e4m3 or int8 (per-token scales), as fa_fwd_varlen.
+ *  causal, window, score_mod   as fa_fwd_varlen.
+ *  launch        workspace of fa_shared_prefix_workspace_bytes() bytes,
+ *                256-byte aligned, for the partials; flags 0.
+ * Three kernels: the prefix pass, the sequences' own keys, the merge.
+ * FA_ERR_UNSUPPORTED for packed K/V, the 5-D pages, other head dims or more
+ * query rows; other errors as fa_fwd_varlen.  A page id outside the pool
+ * counts as a page of zeros; where the prefix pass meets it, it records
+ * FA_ERR_DEVICE_BOUNDS.
+ */
+FA_API fa_status_t fa_fwd_shared_prefix(const fa_tensor_t *q, const fa_tensor_t *k_cache, const fa_tensor_t *v_cache,
+                                 const fa_tensor_t *block_table, const fa_tensor_t *cu_seqlens_q,
+                                 const fa_tensor_t *cu_seqlens_k, const fa_tensor_t *k_scale,
+                                 const fa_tensor_t *v_scale, fa_tensor_t *out, fa_tensor_t *lse, float softmax_scale,
+                                 int32_t causal, int32_t window, const fa_score_mod_t *score_mod,
+                                 const fa_shared_prefix_t *prefix, int32_t page_size, const fa_launch_t *launch,
+                                 void *stream);
+
+/* Prepared form (see fa_fwd_plan_create): launched by fa_fwd_plan_launch and
+ * freed by fa_fwd_plan_destroy.  fa_fwd_plan_launch returns
+ * FA_ERR_INVALID_ARG when another device is current than at creation. */
+FA_API fa_status_t fa_shared_prefix_plan_create(const fa_tensor_t *q, const fa_tensor_t *k_cache,
+                                         const fa_tensor_t *v_cache, const fa_tensor_t *block_table,
+                                         const fa_tensor_t *cu_seqlens_q, const fa_tensor_t *cu_seqlens_k,
+                                         const fa_tensor_t *k_scale, const fa_tensor_t *v_scale, fa_tensor_t *out,
+                                         fa_tensor_t *lse, float softmax_scale, int32_t causal, int32_t window,
+                                         const fa_score_mod_t *score_mod, const fa_shared_prefix_t *prefix,
+                                         int32_t page_size, const fa_launch_t *launch, fa_fwd_plan_t *plan);
+
+/* Workspace bytes of fa_fwd_shared_prefix: fp32 partials [splits, T_q, Hq, D]
+ * and LSEs [splits, Hq, T_q], each 256-byte aligned, of prefix->num_splits +
+ * launch->num_splits splits. */
+FA_API size_t fa_shared_prefix_workspace_bytes(const fa_launch_t *launch, const fa_shared_prefix_t *prefix, int32_t hq,
+                                        int32_t dv);
+
+/* Recommended number of key ranges of the prefix pass (>= 1). */
+FA_API int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq,
+                                        int32_t hkv);
+
+/*
+ * fa_key_weights -- the attention weight that each key received, summed over
+ * query rows and over the heads that share a kv head, from the forward's LSE:
+ *   out[b][hk][j] = beta * weights[b][hk][j]
+ *                   + sum_{i, h in group(hk)} exp(s_ij - lse[h][i])
+ * over the rows i of sequence b that see key j (s_ij, causal, window and
+ * score_mod as in the fa_fwd_varlen call that wrote lse).  It is the score by
+ * which fa_cache_evict chooses; accumulate over decode steps with beta = 1 (or
+ * a decay below 1) and out = weights.
+ *
+ *  q            bf16 [T_q, Hq, Dk], Dk in {64, 128, 192}, Hq/Hkv <= 128.
+ *  k_cache      as fa_fwd_varlen: packed or token-major pages of 1 ... 1024
+ *               keys; bf16, or e4m3 / int8 with k_scale.
+ *  lse          fp32 [Hq, T_q] contiguous, natural log; rows with -inf add
+ *               nothing.
+ *  weights      fp32 [num_seqs, Hkv, L], last dim contiguous, or NULL (as
+ *               beta = 0: nothing is read).
+ *  beta         finite; 0 reads nothing.
+ *  out          fp32 [num_seqs, Hkv, L], last dim contiguous, rows apart from
+ *               each other, L >= launch->max_seqlen_k; `weights` itself (same
+ *               address and strides) or no overlap with it.  Entries j past a
+ *               sequence's keys get beta * weights (0 without weights).
+ *  launch       num_seqs, max_seqlen_q, max_seqlen_k, total_q (and total_k
+ *               for packed K); no workspace.  max_seqlen_k and max_seqlen_q
+ *               bound the lengths: a longer sequence records
+ *               FA_ERR_DEVICE_BOUNDS and its excess is left out.
+ * One kernel: for max_seqlen_q * Hq/Hkv <= 16 bound by reading K, otherwise
+ * tensor-core tiles.  Sums are fp32 in a fixed order (the same bits each run).
+ */
+FA_API fa_status_t fa_key_weights(const fa_tensor_t *q, const fa_tensor_t *k_cache, const fa_tensor_t *block_table,
+                           const fa_tensor_t *cu_seqlens_q, const fa_tensor_t *cu_seqlens_k, const fa_tensor_t *k_scale,
+                           const fa_tensor_t *lse, const fa_tensor_t *weights, float beta, fa_tensor_t *out,
+                           float softmax_scale, int32_t causal, int32_t window, const fa_score_mod_t *score_mod,
+                           int32_t page_size, const fa_launch_t *launch, void *stream);
+
+/* Prepared form, as fa_shared_prefix_plan_create. */
+FA_API fa_status_t fa_key_weights_plan_create(const fa_tensor_t *q, const fa_tensor_t *k_cache,
+                                       const fa_tensor_t *block_table, const fa_tensor_t *cu_seqlens_q,
+                                       const fa_tensor_t *cu_seqlens_k, const fa_tensor_t *k_scale,
+                                       const fa_tensor_t *lse, const fa_tensor_t *weights, float beta, fa_tensor_t *out,
+                                       float softmax_scale, int32_t causal, int32_t window,
+                                       const fa_score_mod_t *score_mod, int32_t page_size, const fa_launch_t *launch,
+                                       fa_fwd_plan_t *plan);
+
+/*
+ * fa_cache_evict -- shortens the sequences of a paged cache to `budget` keys
+ * per kv head, by accumulated attention weight (fa_key_weights).
+ *
+ * A sequence of at most `budget` keys keeps them all.  A longer one keeps, for
+ * each kv head on its own, its first `sink` keys, its last `recent` keys and,
+ * of the others, the budget - sink - recent with the largest weights (ties:
+ * the lowest index; NaN ranks below every number).  The keys that stay keep
+ * their order and become keys 0 ... n - 1: their K and V rows, scales and
+ * weights move, everything else in the pages stays as it was.  All heads keep
+ * the same number, so the new lengths serve every later call; positions that
+ * were encoded into K beforehand stay with the keys.
+ *
+ *  weights           fp32 [num_seqs, Hkv, L], last dim contiguous, L >=
+ *                    launch->max_seqlen_k.
+ *  weights_out       NULL: weights themselves are updated; or fp32 [num_seqs,
+ *                    Hkv, >= budget], last dim contiguous, no overlap with
+ *                    weights.  Entries past the kept keys are set to 0, so that
+ *                    appended keys start from 0.
+ *  k_cache, v_cache  token-major pages [N_pg, P_s, Hkv, D], (Dk, Dv) and types
+ *                    as fa_fwd_varlen; k_scale, v_scale [N_pg, P_s, Hkv] with
+ *                    byte caches.
+ *  block_table       int32 [num_seqs, max_pages].
+ *  block_table_out   NULL: in place; or int32 [num_seqs, >= ceil(budget /
+ *                    page_size)]: the kept keys are written to these pages of
+ *                    the pool, which no block_table row may hold, and the old
+ *                    pages stay as they were.
+ *  cu_seqlens_k      int32 [num_seqs + 1];  cu_seqlens_k_out the same shape, the
+ *                    prefix sums of the new lengths; no overlap.
+ *  kept              int32 [num_seqs, Hkv, budget] contiguous: the old index of
+ *                    each kept key, ascending; -1 past the kept keys.
+ *  budget >= 1, sink >= 0, recent >= 0, sink + recent <= budget.
+ *  launch            num_seqs, max_seqlen_k; no workspace.  A sequence longer
+ *                    than max_seqlen_k, L or its table records
+ *                    FA_ERR_DEVICE_BOUNDS and counts as that long.
+ * In place, sequences may share pages only within their first `sink` keys
+ * (those never move).  A page id outside the pool is skipped and records
+ * FA_ERR_DEVICE_BOUNDS.
+ */
+FA_API fa_status_t fa_cache_evict(const fa_tensor_t *weights, fa_tensor_t *weights_out, const fa_tensor_t *k_cache,
+                           const fa_tensor_t *v_cache, const fa_tensor_t *k_scale, const fa_tensor_t *v_scale,
+                           const fa_tensor_t *block_table, const fa_tensor_t *block_table_out,
+                           const fa_tensor_t *cu_seqlens_k, fa_tensor_t *cu_seqlens_k_out, fa_tensor_t *kept,
+                           int32_t budget, int32_t sink, int32_t recent, int32_t page_size, const fa_launch_t *launch,
+                           void *stream);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 FA_API const char *fa_last_error(void);
