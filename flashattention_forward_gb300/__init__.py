@@ -9,10 +9,10 @@ library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -158,8 +158,9 @@ def lib() -> ctypes.CDLL:
             L.fa_bwd_varlen.restype = ctypes.c_int
             L.fa_bwd_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32]
             L.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
+            # their fa_tensor_t arguments are given as packed bytes (_packer)
             i32, f32, ptr = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
-            L.fa_fwd_shared_prefix.argtypes = [P(Tensor)] * 10 + [f32, i32, i32, P(ScoreMod), P(SharedPrefix), i32,
+            L.fa_fwd_shared_prefix.argtypes = [ptr] * 10 + [f32, i32, i32, P(ScoreMod), P(SharedPrefix), i32,
                                                                  P(Launch), ptr]
             L.fa_fwd_shared_prefix.restype = ctypes.c_int
             L.fa_shared_prefix_plan_create.argtypes = L.fa_fwd_shared_prefix.argtypes[:-1] + [P(ptr)]
@@ -168,11 +169,11 @@ def lib() -> ctypes.CDLL:
             L.fa_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
             L.fa_shared_prefix_default_splits.argtypes = [ctypes.c_int64, i32, i32, i32, i32]
             L.fa_shared_prefix_default_splits.restype = i32
-            L.fa_key_weights.argtypes = [P(Tensor)] * 8 + [f32, P(Tensor), f32, i32, i32, P(ScoreMod), i32, P(Launch), ptr]
+            L.fa_key_weights.argtypes = [ptr] * 8 + [f32, ptr, f32, i32, i32, P(ScoreMod), i32, P(Launch), ptr]
             L.fa_key_weights.restype = ctypes.c_int
             L.fa_key_weights_plan_create.argtypes = L.fa_key_weights.argtypes[:-1] + [P(ptr)]
             L.fa_key_weights_plan_create.restype = ctypes.c_int
-            L.fa_cache_evict.argtypes = [P(Tensor)] * 11 + [i32] * 4 + [P(Launch), ptr]
+            L.fa_cache_evict.argtypes = [ptr] * 11 + [i32] * 4 + [P(Launch), ptr]
             L.fa_cache_evict.restype = ctypes.c_int
             _lib = L
     return _lib
@@ -496,25 +497,41 @@ def bwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
 
 # ------------------------------------------------- around the paged decode --
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """Make ``device`` and ``stream`` (None: the device's current stream)
-    current, so that what a call allocates belongs to the stream it runs on;
-    yields the stream's handle."""
+def _run_on(device: torch.device, stream, body):
+    """body(stream handle) with ``device`` and ``stream`` (None: the device's
+    current stream) current, so that what it allocates belongs to the stream
+    it runs on."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
+    if stream is None and torch.cuda.current_device() == device.index:
+        return body(torch.cuda.current_stream(device.index).cuda_stream)
     with torch.cuda.device(device):
         if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
 
 
-def _same_device(device: torch.device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
+_TENSOR = struct.Struct("@Pii5q5q")     # fa_tensor_t
+assert _TENSOR.size == ctypes.sizeof(Tensor)
+_PAD = [(0,) * (5 - n) for n in range(6)]
+
+
+def _packer(device: torch.device):
+    """pack(tensor, fa dtype or None) -> its fa_tensor_t as bytes (None for
+    None); every tensor has to be on ``device``."""
+    index = device.index
+
+    def pack(t, fa_dtype=None):
+        if t is None:
+            return None
+        if t.get_device() != index:
             raise ValueError(f"all tensors must be on {device}, one is on {t.device}")
+        shape = t.shape
+        pad = _PAD[len(shape)]
+        return _TENSOR.pack(t.data_ptr(), _DT[t.dtype] if fa_dtype is None else fa_dtype, len(shape), *shape, *pad,
+                            *t.stride(), *pad)
+    return pack
 
 
 class _Prepared:
@@ -565,8 +582,10 @@ def _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, *, max_
     Tq, Hq, D = q.shape
     Hkv, Dv = _cache_dims(k_cache, v_cache)
     kv_dt = _kv_dtype(k_cache)
-    _same_device(q.device, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_table, cu_groups, prefix_lens, k_scale,
-                 v_scale, out, lse, workspace)
+    pack = _packer(q.device)
+    for t in (cu_groups, prefix_lens, workspace):
+        if t is not None and t.device != q.device:
+            raise ValueError(f"all tensors must be on {q.device}, one is on {t.device}")
     for name, t, n in (("cu_groups", cu_groups, None), ("prefix_lens", prefix_lens, cu_groups.shape[0] - 1)):
         if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
             raise ValueError(f"{name} must be contiguous int32: cu_groups [G + 1], prefix_lens [G]")
@@ -594,11 +613,9 @@ def _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, *, max_
         launch.workspace = workspace.data_ptr()
         launch.workspace_bytes = workspace.numel() * workspace.element_size()
     sm = ScoreMod(kind=score_mod, alibi_slope=alibi_slope, softcap=softcap)
-    descs = [as_tensor(q), as_tensor(k_cache, kv_dt), as_tensor(v_cache, kv_dt), as_tensor(block_table),
-             as_tensor(cu_seqlens_q), as_tensor(cu_seqlens_k), as_tensor(k_scale), as_tensor(v_scale), as_tensor(out),
-             as_tensor(lse)]
-    args = [_ref(a) for a in descs] + [float(softmax_scale), int(bool(causal)), int(window), ctypes.byref(sm),
-                                       ctypes.byref(prefix), int(page_size), ctypes.byref(launch)]
+    args = [pack(q), pack(k_cache, kv_dt), pack(v_cache, kv_dt), pack(block_table), pack(cu_seqlens_q),
+            pack(cu_seqlens_k), pack(k_scale), pack(v_scale), pack(out), pack(lse), float(softmax_scale),
+            int(bool(causal)), int(window), ctypes.byref(sm), ctypes.byref(prefix), int(page_size), ctypes.byref(launch)]
     keep = [q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_table, cu_groups, prefix_lens, k_scale, v_scale, out,
             lse, workspace]
     return args, keep, (out, lse)
@@ -621,10 +638,11 @@ def fwd_shared_prefix(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     alibi_slope, softcap, out, lse, return_lse, workspace, and the split counts
     prefix_splits and num_splits (None: the library's choice).  Returns
     ``(out [T_q, Hq, D] bf16, lse [Hq, T_q] fp32 or None)``."""
-    with _on(q.device, stream) as s:
+    def call(s):
         args, _keep, result = _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw)
         _check(lib().fa_fwd_shared_prefix(*args, s))
-    return result
+        return result
+    return _run_on(q.device, stream, call)
 
 
 class SharedPrefixPlan(_Prepared):
@@ -634,11 +652,12 @@ class SharedPrefixPlan(_Prepared):
     run.  Two runs at once on different streams would race on the workspace."""
 
     def __init__(self, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw):
-        with _on(q.device, None):
+        def create(_s):
             args, keep, result = _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, **kw)
             handle = ctypes.c_void_p(0)
             _check(lib().fa_shared_prefix_plan_create(*args, ctypes.byref(handle)))
-            super().__init__(q.device, keep, result, handle)
+            super(SharedPrefixPlan, self).__init__(q.device, keep, result, handle)
+        _run_on(q.device, None, create)
 
 
 def _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen_q, max_seqlen_k, weights=None, beta=1.0,
@@ -646,7 +665,7 @@ def _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen
                       causal=False, window=0, score_mod=MOD_NONE, alibi_slope=0.0, softcap=0.0):
     B = cu_seqlens_q.shape[0] - 1
     Tq, _Hq, D = q.shape
-    _same_device(q.device, k_cache, lse, cu_seqlens_q, cu_seqlens_k, weights, out, block_table, k_scale)
+    pack = _packer(q.device)
     if out is None:
         out = weights
     if out is None:
@@ -658,11 +677,9 @@ def _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, *, max_seqlen
     launch = Launch(num_seqs=B, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, num_splits=0, total_q=Tq,
                     total_k=total_k)
     sm = ScoreMod(kind=score_mod, alibi_slope=alibi_slope, softcap=softcap)
-    descs = [as_tensor(q), as_tensor(k_cache, _kv_dtype(k_cache)), as_tensor(block_table), as_tensor(cu_seqlens_q),
-             as_tensor(cu_seqlens_k), as_tensor(k_scale), as_tensor(lse), as_tensor(weights)]
-    args = [_ref(a) for a in descs] + [float(beta), ctypes.byref(as_tensor(out)), float(softmax_scale),
-                                       int(bool(causal)), int(window), ctypes.byref(sm), int(page_size),
-                                       ctypes.byref(launch)]
+    args = [pack(q), pack(k_cache, _kv_dtype(k_cache)), pack(block_table), pack(cu_seqlens_q), pack(cu_seqlens_k),
+            pack(k_scale), pack(lse), pack(weights), float(beta), pack(out), float(softmax_scale), int(bool(causal)),
+            int(window), ctypes.byref(sm), int(page_size), ctypes.byref(launch)]
     return args, [q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, weights, out, block_table, k_scale], out
 
 
@@ -680,10 +697,11 @@ def key_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, cu_se
     max_seqlen_k]); block_table and page_size for paged keys; total_k, k_scale,
     softmax_scale, causal, window, score_mod, alibi_slope, softcap as in the
     forward call that wrote ``lse``.  Returns ``out``."""
-    with _on(q.device, stream) as s:
+    def call(s):
         args, _keep, out = _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw)
         _check(lib().fa_key_weights(*args, s))
-    return out
+        return out
+    return _run_on(q.device, stream, call)
 
 
 class KeyWeightsPlan(_Prepared):
@@ -691,11 +709,12 @@ class KeyWeightsPlan(_Prepared):
     returns out."""
 
     def __init__(self, q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw):
-        with _on(q.device, None):
+        def create(_s):
             args, keep, out = _key_weights_args(q, k_cache, lse, cu_seqlens_q, cu_seqlens_k, **kw)
             handle = ctypes.c_void_p(0)
             _check(lib().fa_key_weights_plan_create(*args, ctypes.byref(handle)))
-            super().__init__(q.device, keep, out, handle)
+            super(KeyWeightsPlan, self).__init__(q.device, keep, out, handle)
+        _run_on(q.device, None, create)
 
 
 def cache_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cu_seqlens_k: torch.Tensor, *,
@@ -714,18 +733,20 @@ def cache_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     Hkv, budget]: old indices, -1 past the kept keys; cu_seqlens_k_out int32
     [B + 1])``."""
     B, Hkv = weights.shape[0], weights.shape[1]
-    _same_device(weights.device, k_cache, v_cache, cu_seqlens_k, block_table, k_scale, v_scale, block_table_out,
-                 weights_out, kept, cu_seqlens_k_out)
-    with _on(weights.device, stream) as s:
-        if kept is None:
-            kept = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
-        if cu_seqlens_k_out is None:
-            cu_seqlens_k_out = torch.empty((B + 1,), dtype=torch.int32, device=weights.device)
+
+    def call(s):
+        kept_ = kept
+        if kept_ is None:
+            kept_ = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
+        cu_out = cu_seqlens_k_out
+        if cu_out is None:
+            cu_out = torch.empty((B + 1,), dtype=torch.int32, device=weights.device)
         kv_dt = _kv_dtype(k_cache)
         launch = Launch(num_seqs=B, max_seqlen_q=0, max_seqlen_k=max_seqlen_k)
-        descs = [as_tensor(weights), as_tensor(weights_out), as_tensor(k_cache, kv_dt), as_tensor(v_cache, kv_dt),
-                 as_tensor(k_scale), as_tensor(v_scale), as_tensor(block_table), as_tensor(block_table_out),
-                 as_tensor(cu_seqlens_k), as_tensor(cu_seqlens_k_out), as_tensor(kept)]
-        _check(lib().fa_cache_evict(*[_ref(d) for d in descs], int(budget), int(sink), int(recent), int(page_size),
-                                    ctypes.byref(launch), s))
-    return kept, cu_seqlens_k_out
+        pack = _packer(weights.device)
+        _check(lib().fa_cache_evict(pack(weights), pack(weights_out), pack(k_cache, kv_dt), pack(v_cache, kv_dt),
+                                    pack(k_scale), pack(v_scale), pack(block_table), pack(block_table_out),
+                                    pack(cu_seqlens_k), pack(cu_out), pack(kept_), int(budget), int(sink), int(recent),
+                                    int(page_size), ctypes.byref(launch), s))
+        return kept_, cu_out
+    return _run_on(weights.device, stream, call)

@@ -1,6 +1,4 @@
 // Instantiations and launchers of the key-weight kernels (fa_key_weights.cuh).
-#include <climits>
-
 #include "fa_key_weights.cuh"
 #include "fa_internal.h"
 

@@ -24,7 +24,6 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <climits>
 
 #include "fa_decode.cuh"
 #include "sm103_ptx.cuh"
@@ -80,29 +79,21 @@ __device__ __forceinline__ KwSeq kw_sequence(const KeyWeightsParams &p, int b) {
   return s;
 }
 
-// Row of the flat [tokens, Hkv] cache view that holds key j; -1 (flagged) for
-// a page or row outside the cache.
-__device__ __forceinline__ int64_t kw_token(const KeyWeightsParams &p, int b, const KwSeq &s, int j, const uint8_t *&row,
-                                            int hk) {
-  int64_t tok;
-  if (p.block_table) {
-    const int page = __ldg(p.block_table + (int64_t)b * p.bt_stride + (j >> p.page_shift));
-    const int slot = j & (p.page_size - 1);
-    if (page < 0 || page >= p.n_pages) {
-      record_error(p.err, kErrBounds);
-      return -1;
-    }
-    tok = (int64_t)page * p.page_size + slot;
-    row = p.k + (int64_t)page * p.s_page + (int64_t)slot * p.s_slot + (int64_t)hk * p.s_head;
-  } else {
-    tok = (int64_t)s.ka + j;
-    if (tok < 0 || tok >= p.n_pages) {
-      record_error(p.err, kErrBounds);
-      return -1;
-    }
-    row = p.k + tok * p.s_page + (int64_t)hk * p.s_head;
-  }
-  return tok;
+// Page of key j (packed: its row; page_size is then 1).  Looked up for several
+// keys before any is used, so that the reads are in flight together; ids
+// outside the cache are replaced by -1 and flagged by the caller's `bad`.
+__device__ __forceinline__ int kw_page(const KeyWeightsParams &p, const int32_t *bt, int ka, int j, bool live, bool &bad) {
+  if (!live) return -1;
+  const int pg = bt ? __ldg(bt + (j >> p.page_shift)) : ka + j;
+  const bool ok = pg >= 0 && pg < p.n_pages;
+  bad = bad || !ok;
+  return ok ? pg : -1;
+}
+__device__ __forceinline__ const uint8_t *kw_row(const KeyWeightsParams &p, int pg, int j, int hk) {
+  return p.k + (int64_t)pg * p.s_page + (int64_t)(j & (p.page_size - 1)) * p.s_slot + (int64_t)hk * p.s_head;
+}
+__device__ __forceinline__ float kw_scale(const KeyWeightsParams &p, int pg, int j, int hk) {
+  return __ldg(p.k_scale + ((int64_t)pg * p.page_size + (j & (p.page_size - 1))) * p.hkv + hk);
 }
 
 // Entries [lo, hi) that gain nothing: w_out = beta * w_in.
@@ -115,21 +106,29 @@ __device__ __forceinline__ void kw_carry(const KeyWeightsParams &p, int b, int h
 
 __device__ __forceinline__ uint4 kw_ld_stream(const uint8_t *a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(a));
   return v;
 }
 
-// exp2 argument of one pair from the raw product s, factor c (scale, key
-// scale and row factor, in log2 units; soft-cap: in 2u log2(e) units).
-__device__ __forceinline__ float kw_score(const KeyWeightsParams &p, float s, float c, int dist) {
-  if (p.mod == 2) {
-    float r;
-    return softcap_log2_score(ex2(s * c), p.softcap_log2, r);
+// Row i' sees key j iff (unsigned)(i' - j + add) < range, for every mask; a row
+// at kKwHidden sees no key (positions stay below 2^30 in magnitude).
+constexpr int kKwHidden = -(1 << 30) - (1 << 29);
+struct KwVisible {
+  int add;
+  unsigned range;
+};
+__device__ __forceinline__ KwVisible kw_visible(const KeyWeightsParams &p) {
+  KwVisible v;
+  if (p.window > 0) {
+    v.add = p.causal ? 0 : p.window - 1;
+    v.range = p.causal ? (unsigned)p.window : 2u * (unsigned)p.window - 1u;
+  } else {
+    v.add = p.causal ? 0 : 1 << 30;
+    v.range = 1u << 31;
   }
-  if (p.mod == 1) return fmaf(s, c, -p.alibi_log2 * fabsf((float)dist));
-  return s * c;
+  return v;
 }
 
 // --------------------------------------------------------------- rows form --
@@ -137,10 +136,15 @@ constexpr int kKwWarps = 8;
 
 // NT tiles of 8 query rows.
 template <int D, int KV, int NT>
-__global__ void __launch_bounds__(kKwWarps * 32) fa_key_weights_rows_kernel(const KeyWeightsParams p) {
+__global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(const KeyWeightsParams p) {
   constexpr int ESZ = KV ? 1 : 2;
   constexpr int NP = D * ESZ / 64;            // 16-byte pieces of a key row per lane
-  constexpr int U = NP * 4 <= 16 ? 2 : 1;     // 16-key groups per warp step: up to 64 registers of keys in flight
+  // 16-key groups per warp step, 2 to 4 KB of keys.  The next step's are loaded
+  // while this one's are used (AHEAD), so that every warp always has keys in
+  // flight, where two steps' keys and the query fragments fit the registers of
+  // two CTAs per SM.
+  constexpr int U = (NP == 1 ? 4 : (NP == 2 ? 2 : 1)) > NT ? (NP == 1 ? 4 : (NP == 2 ? 2 : 1)) / NT : 1;
+  constexpr bool AHEAD = NP * U <= 4 && NT * D <= 192;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hk = blockIdx.y, b = blockIdx.z;
   const KwSeq sq_ = kw_sequence(p, b);
@@ -214,8 +218,9 @@ __global__ void __launch_bounds__(kKwWarps * 32) fa_key_weights_rows_kernel(cons
       }
     }
   }
-  // The rows of this lane's C columns, 8 nt + 2t + e: -LSE (log2 units), i',
-  // and the score factor.  Rows that see nothing (LSE -inf) weigh nothing.
+  // The rows of this lane's C columns, 8 nt + 2t + e: -LSE (log2 units), i'
+  // (relative to key lo + g, with the mask's offset) and the score factor.  Rows that see nothing (LSE -inf) weigh nothing.
+  const KwVisible vb = kw_visible(p);
   float nl[NT][2], sc[NT][2];
   int ip[NT][2];
 #pragma unroll
@@ -226,30 +231,65 @@ __global__ void __launch_bounds__(kKwWarps * 32) fa_key_weights_rows_kernel(cons
       const float f = __shfl_sync(0xffffffffu, inv[nt], (2 * t + e) * 4);
       sc[nt][e] = (p.mod == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * f;
       nl[nt][e] = -INFINITY;
-      ip[nt][e] = 0;
+      ip[nt][e] = kKwHidden;
       if (r < rows) {
         const float l = __ldg(p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + sq_.qa + r / p.group);
         nl[nt][e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        ip[nt][e] = r / p.group + sq_.shift;
+        ip[nt][e] = r / p.group + sq_.shift + vb.add - lo - g;
       }
     }
 
   const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
   float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
-  for (int base = lo + warp * 16 * U; base < hi; base += kKwWarps * 16 * U) {
-    uint4 kr[2 * U][NP];
-    float ks[2 * U];
-    bool live[2 * U];
+  const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
+  // the lane's key rows of a step are base + 8 u + g; their pages are read one step ahead
+  bool bad = false;
+  int pgn[2 * U];
+  auto pages = [&](int base) {
 #pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {         // the lane's key rows: base + 8 u + g
+    for (int u = 0; u < 2 * U; ++u) {
       const int j = base + 8 * u + g;
-      const uint8_t *row = p.k;
-      int64_t tok = -1;
-      if (j < hi) tok = kw_token(p, b, sq_, j, row, hk);
-      live[u] = tok >= 0;
-      ks[u] = (KV && live[u]) ? __ldg(p.k_scale + tok * p.hkv + hk) : 1.f;
+      pgn[u] = kw_page(p, bt, sq_.ka, j, j < hi, bad);
+    }
+  };
+  uint4 kr[2 * U][NP], kn[2 * U][NP];
+  float ks[2 * U], ksn[2 * U];
+  unsigned dead = 0, deadn = 0;               // bit u: the page of key base + 8 u + g is not in the pool
+  auto load = [&](int base) {
+    deadn = 0;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) kr[u][i] = live[u] ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 2 * U; ++u) {
+      const int j = base + 8 * u + g;
+      const bool live = pgn[u] >= 0;
+      const uint8_t *row = kw_row(p, max(pgn[u], 0), j, hk);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kn[u][i] = live ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
+      ksn[u] = (KV && live) ? kw_scale(p, pgn[u], j, hk) : 1.f;
+      if (!live) deadn |= 1u << u;
+    }
+  };
+  const int step = kKwWarps * 16 * U;
+  int base = lo + warp * 16 * U;
+  pages(base);
+  if (AHEAD) {
+    load(base);
+    pages(base + step);
+  }
+  for (; base < hi; base += step) {
+    if (!AHEAD) {
+      load(base);
+      pages(base + step);
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * U; ++u) {
+      ks[u] = ksn[u];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kr[u][i] = kn[u][i];
+    }
+    dead = deadn;
+    if (AHEAD && base + step < hi) {
+      load(base + step);
+      pages(base + 2 * step);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -280,25 +320,31 @@ __global__ void __launch_bounds__(kKwWarps * 32) fa_key_weights_rows_kernel(cons
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {           // keys base + 16 u + 8 x + g
-        const int j = base + 16 * u + 8 * x + g;
+        const int rel = base - lo + 16 * u + 8 * x, j = lo + rel + g;
         float sum = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int d = ip[nt][e] - j;
-            bool vis = live[2 * u + x] && nt * 8 + 2 * t + e < rows;
-            if (p.causal) vis = vis && d >= 0;
-            if (p.window > 0) vis = vis && (p.causal ? d < p.window : abs(d) < p.window);
-            const float y = kw_score(p, c[nt][2 * x + e], sc[nt][e] * ks[2 * u + x], d) + nl[nt][e];
-            sum += vis ? ex2(y) : 0.f;
+            const int d = ip[nt][e] - rel;    // i' - j + the mask's offset
+            float y = c[nt][2 * x + e] * (KV ? sc[nt][e] * ks[2 * u + x] : sc[nt][e]);
+            if (p.mod == 2) {
+              float r;
+              y = softcap_log2_score(ex2(y), p.softcap_log2, r);
+            } else if (p.mod == 1) {
+              y = fmaf(-p.alibi_log2, fabsf((float)(d - vb.add)), y);
+            }
+            y = ex2(y + nl[nt][e]);
+            sum += (unsigned)d < vb.range ? y : 0.f;
           }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (dead & (1u << (2 * u + x))) sum = 0.f;
         if (t == 0 && j < hi) wo[j] = wi ? fmaf(p.beta, wi[j], sum) : sum;
       }
     }
   }
+  if (bad) record_error(p.err, kErrBounds);
 }
 
 // --------------------------------------------------------------- tile form --
@@ -310,9 +356,12 @@ struct KwTileCfg {
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = KC * kChunkBytes;
   static constexpr int kOffCol = kOffQ + NCH * kChunkBytes;   // [2][128] -LSE, [2][128] i'
-  static constexpr int kOffBar = kOffCol + 2 * 128 * 8;
-  static constexpr int kSmemBytes = kOffBar + (2 * NCH + 4) * 8 + 16 + 1024;
-  static constexpr int kThreads = 6 * 32;
+  static constexpr int kOffSum = kOffCol + 2 * 128 * 8;       // [128] the second warpgroup's sums
+  static constexpr int kOffBar = kOffSum + 128 * 4;
+  static constexpr int kSmemBytes = kOffBar + (2 * NCH + 5) * 8 + 16 + 1024;
+  // two warpgroups take the tiles in turn, then the producer and the MMA warp
+  static constexpr int kThreads = 10 * 32, kFill = 9 * 32;
+  static constexpr int kProducerWarp = 8, kMmaWarp = 9;
   static constexpr uint32_t kTmemCols = 256;        // two S^T tiles
   static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
 };
@@ -340,9 +389,11 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = blockIdx.y, b = blockIdx.z;
+  // key tiles in the slowest grid dimension: under a causal mask the first
+  // tiles of every sequence have the most queries, and so start first
+  const int hk = blockIdx.x, b = blockIdx.y;
   const KwSeq s = kw_sequence(p, b);
-  const int64_t j0_64 = (int64_t)blockIdx.x * 128;
+  const int64_t j0_64 = (int64_t)blockIdx.z * 128;
   if (s.sq <= 0 || j0_64 >= s.sk) {
     kw_carry(p, b, hk, j0_64, min(p.extent, j0_64 + 128));
     return;
@@ -366,8 +417,8 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
   float *col_nl = reinterpret_cast<float *>(smem + Cfg::kOffCol);      // [2][128]
   int *col_ip = reinterpret_cast<int *>(col_nl + 256);                 // [2][128]
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
-  uint64_t *q_empty = q_full + NCH, *s_full = q_empty + NCH, *s_empty = s_full + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_empty + 2);
+  uint64_t *q_empty = q_full + NCH, *s_full = q_empty + NCH, *s_empty = s_full + 2, *k_ready = s_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(k_ready + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int rows_box = tpt * p.group;               // rows of a Q tile, at most 128
   if (threadIdx.x == 0) {
@@ -379,52 +430,75 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       mbar_init(smem_u32(s_full + i), 1);
       mbar_init(smem_u32(s_empty + i), 128);
     }
+    mbar_init(smem_u32(k_ready), Cfg::kFill);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == Cfg::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
-  // rows that no box writes (128 % group != 0) stay zero
-  for (int e = threadIdx.x; e < NCH * (128 - rows_box) * 8; e += Cfg::kThreads) {
-    const int ch = e / ((128 - rows_box) * 8), rest = e % ((128 - rows_box) * 8);
-    *reinterpret_cast<uint4 *>(sQ + ch * Cfg::kChunkBytes + rows_box * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
-  }
-  // The key tile as the K-major, 128-byte-swizzled A operand in bf16: any page
-  // size, and byte caches exactly (their scale multiplies the key's sum
-  // argument below).  Rows past the sequence are zero.
-  if (p.kv == 0) {
-    constexpr int PR = D / 8;                       // 16-byte pieces of a row
-    for (int e = threadIdx.x; e < 128 * PR; e += Cfg::kThreads) {
-      const int r = e / PR, c = e % PR, j = j0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const uint8_t *row;
-      if (j < s.sk && kw_token(p, b, s, j, row, hk) >= 0) v = kw_ld_stream(row + c * 16);
-      *reinterpret_cast<uint4 *>(sK + (c >> 3) * Cfg::kChunkBytes + sw128(r, c & 7)) = v;
-    }
-  } else {
-    constexpr int PR = D / 16;
-    for (int e = threadIdx.x; e < 128 * PR; e += Cfg::kThreads) {
-      const int r = e / PR, c = e % PR, j = j0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const uint8_t *row;
-      if (j < s.sk && kw_token(p, b, s, j, row, hk) >= 0) v = kw_ld_stream(row + c * 16);
-      const uint2 lo = make_uint2(v.x, v.y), hi = make_uint2(v.z, v.w);
-      uint8_t *dst = sK + (c >> 2) * Cfg::kChunkBytes;
-      const int c8 = (2 * c) & 7;
-      *reinterpret_cast<uint4 *>(dst + sw128(r, c8)) = p.kv == 1 ? kw_bytes8_to_bf16<1>(lo) : kw_bytes8_to_bf16<2>(lo);
-      *reinterpret_cast<uint4 *>(dst + sw128(r, c8 + 1)) =
-          p.kv == 1 ? kw_bytes8_to_bf16<1>(hi) : kw_bytes8_to_bf16<2>(hi);
-    }
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
 
-  if (warp == 4) {
+  if (warp != Cfg::kProducerWarp) {
+    // The key tile as the K-major, 128-byte-swizzled A operand in bf16: any
+    // page size, and byte caches exactly (their scale multiplies the key's sum
+    // argument below).  Rows past the sequence are zero.  While the producer's
+    // first query tiles are under way, the other nine warps read the keys,
+    // every piece of a thread before it stores any.
+    const int ft = warp == Cfg::kMmaWarp ? 256 + lane : (int)threadIdx.x;   // 0 ... kFill - 1
+    constexpr int FT = Cfg::kFill;
+    bool bad = false;
+    if (p.kv == 0) {
+      constexpr int PR = D / 8, N = (128 * PR + FT - 1) / FT;   // 16-byte pieces of a row, of a thread
+      uint4 v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = ft + i * FT, r = e / PR, j = j0 + r;
+        const int pg = kw_page(p, bt, s.ka, j, e < 128 * PR && j < s.sk, bad);
+        v[i] = pg >= 0 ? kw_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = ft + i * FT, r = e / PR, c = e % PR;
+        if (e < 128 * PR) *reinterpret_cast<uint4 *>(sK + (c >> 3) * Cfg::kChunkBytes + sw128(r, c & 7)) = v[i];
+      }
+    } else {
+      constexpr int PR = D / 16, N = (128 * PR + FT - 1) / FT;
+      uint4 v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = ft + i * FT, r = e / PR, j = j0 + r;
+        const int pg = kw_page(p, bt, s.ka, j, e < 128 * PR && j < s.sk, bad);
+        v[i] = pg >= 0 ? kw_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = ft + i * FT, r = e / PR, c = e % PR;
+        if (e >= 128 * PR) continue;
+        const uint2 lo = make_uint2(v[i].x, v[i].y), hi = make_uint2(v[i].z, v[i].w);
+        uint8_t *dst = sK + (c >> 2) * Cfg::kChunkBytes;
+        const int c8 = (2 * c) & 7;
+        *reinterpret_cast<uint4 *>(dst + sw128(r, c8)) = p.kv == 1 ? kw_bytes8_to_bf16<1>(lo) : kw_bytes8_to_bf16<2>(lo);
+        *reinterpret_cast<uint4 *>(dst + sw128(r, c8 + 1)) =
+            p.kv == 1 ? kw_bytes8_to_bf16<1>(hi) : kw_bytes8_to_bf16<2>(hi);
+      }
+    }
+    if (bad) record_error(p.err, kErrBounds);
+    // rows of the query tiles that no box writes (128 % group != 0) stay zero
+    for (int e = ft; e < NCH * (128 - rows_box) * 8; e += FT) {
+      const int ch = e / ((128 - rows_box) * 8), rest = e % ((128 - rows_box) * 8);
+      *reinterpret_cast<uint4 *>(sQ + ch * Cfg::kChunkBytes + rows_box * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(k_ready));
+  }
+
+  if (warp == Cfg::kProducerWarp) {
     // ------------------------------------------------------- producer --
     if (lane == 0) {
       prefetch_tmap(&tm_q);
@@ -440,9 +514,9 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
                       s.qa + t_lo + it * tpt);
         }
       // the last loads have landed before the CTA ends, whatever the others do
-      for (int i = max(0, n - NCH); i < n; ++i) mbar_wait(smem_u32(q_full + i % NCH), (i / NCH) & 1, abort_flag, p.err);
+      for (int i = max(0, n - NCH); i < n; ++i) mbar_drain(smem_u32(q_full + i % NCH), (i / NCH) & 1);
     }
-  } else if (warp == 5) {
+  } else if (warp == Cfg::kMmaWarp) {
     // ----------------------------------------------------------- MMAs --
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
@@ -450,7 +524,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       const uint32_t hi = (uint32_t)(dk >> 32), lo_k = (uint32_t)dk;
       const uint32_t lo_q = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
       int n = 0;
-      bool ok = true;
+      bool ok = mbar_wait(smem_u32(k_ready), 0, abort_flag, p.err);
       for (int it = 0; ok && it < n_tiles; ++it) {
         const int x = it & 1;
         if (it >= 2 && !(ok = mbar_wait(smem_u32(s_empty + x), ((it >> 1) - 1) & 1, abort_flag, p.err))) break;
@@ -475,41 +549,44 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
     }
   } else {
     // --------------------------------------------- one key per thread --
-    const int r = threadIdx.x, j = j0 + r;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    // Warpgroup x takes the tiles x, x + 2, ...: the tiles of S^T buffer x.
+    const int x = warp >> 2, r = threadIdx.x & 127, j = j0 + r;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     float ks = 1.f;
-    if (p.kv && j < s.sk) {
-      const uint8_t *row;
-      const int64_t tok = kw_token(p, b, s, j, row, hk);
-      if (tok >= 0) ks = __ldg(p.k_scale + tok * p.hkv + hk);
+    if (p.kv) {
+      bool bad = false;
+      const int pg = kw_page(p, bt, s.ka, j, j < s.sk, bad);
+      if (pg >= 0) ks = kw_scale(p, pg, j, hk);
     }
     const float c = (MOD == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * ks;
+    const KwVisible vb = kw_visible(p);
     // column r of a tile: token t_lo + it * tpt + r / group, head r % group
-    const int ctok = r / p.group;
+    const int ctok = t_lo + r / p.group;
     const float *lse_r = p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + s.qa;
+    float *nl_buf = col_nl + x * 128;
+    int *ip_buf = col_ip + x * 128;                 // i' - j0 + the mask's offset
     auto column = [&](int it, float &nl, int &ip) {
-      const int tok = t_lo + it * tpt + ctok;
+      const int tok = ctok + it * tpt;
       nl = -INFINITY;
-      ip = INT_MIN / 2;                             // hidden from every key
+      ip = kKwHidden;
       if (it < n_tiles && r < rows_box && tok < t_hi) {
         const float l = __ldg(lse_r + tok);
         nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        ip = tok + s.shift;
+        ip = tok + s.shift - j0 + vb.add;
       }
     };
     float nl_next;
     int ip_next;
-    column(0, nl_next, ip_next);
+    column(x, nl_next, ip_next);
     float total = 0.f;
     bool ok = true;
-    for (int it = 0; it < n_tiles; ++it) {
-      const int x = it & 1;
-      // this tile's column constants; the buffer's last readers passed the
-      // previous tile's barrier
-      col_nl[x * 128 + r] = nl_next;
-      col_ip[x * 128 + r] = ip_next;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      column(it + 1, nl_next, ip_next);
+    for (int it = x; it < n_tiles; it += 2) {
+      // this tile's column constants, between the barriers of its readers
+      if (it >= 2) asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+      nl_buf[r] = nl_next;
+      ip_buf[r] = ip_next;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+      column(it + 2, nl_next, ip_next);
       const int ta = t_lo + it * tpt, tb = min(ta + tpt, t_hi) - 1;    // first and last token of the tile
       bool mask = tb - ta + 1 < tpt;                 // rows of other sequences may hold anything
       if (p.causal) mask = mask || ta + s.shift < jl;
@@ -527,8 +604,8 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
           tc_fence_before();
           mbar_arrive(smem_u32(s_empty + x));
         }
-        const float4 *nl4 = reinterpret_cast<const float4 *>(col_nl + x * 128 + q * 32);
-        const int4 *ip4 = reinterpret_cast<const int4 *>(col_ip + x * 128 + q * 32);
+        const float4 *nl4 = reinterpret_cast<const float4 *>(nl_buf + q * 32);
+        const int4 *ip4 = reinterpret_cast<const int4 *>(ip_buf + q * 32);
         if constexpr (MOD == 2) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], c);
@@ -550,10 +627,11 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
             float4 n = nl4[e >> 2];
             if constexpr (MOD == 1) {
               const int4 i = ip4[e >> 2];
-              n.x = fmaf(-p.alibi_log2, fabsf((float)(i.x - j)), n.x);
-              n.y = fmaf(-p.alibi_log2, fabsf((float)(i.y - j)), n.y);
-              n.z = fmaf(-p.alibi_log2, fabsf((float)(i.z - j)), n.z);
-              n.w = fmaf(-p.alibi_log2, fabsf((float)(i.w - j)), n.w);
+              const int o = r + vb.add;              // distance i' - j = i - o
+              n.x = fmaf(-p.alibi_log2, fabsf((float)(i.x - o)), n.x);
+              n.y = fmaf(-p.alibi_log2, fabsf((float)(i.y - o)), n.y);
+              n.z = fmaf(-p.alibi_log2, fabsf((float)(i.z - o)), n.z);
+              n.w = fmaf(-p.alibi_log2, fabsf((float)(i.w - o)), n.w);
             }
             fma2v(v[e], v[e + 1], c, n.x, n.y);
             fma2v(v[e + 2], v[e + 3], c, n.z, n.w);
@@ -563,14 +641,10 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const int4 i = ip4[e >> 2];
-            const int ii[4] = {i.x, i.y, i.z, i.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              bool vis = ii[k] > INT_MIN / 4;
-              if (p.causal) vis = vis && j <= ii[k];
-              if (p.window > 0) vis = vis && (p.causal ? ii[k] - j < p.window : abs(ii[k] - j) < p.window);
-              v[e + k] = vis ? v[e + k] : -INFINITY;
-            }
+            v[e] = (unsigned)(i.x - r) < vb.range ? v[e] : -INFINITY;
+            v[e + 1] = (unsigned)(i.y - r) < vb.range ? v[e + 1] : -INFINITY;
+            v[e + 2] = (unsigned)(i.z - r) < vb.range ? v[e + 2] : -INFINITY;
+            v[e + 3] = (unsigned)(i.w - r) < vb.range ? v[e + 3] : -INFINITY;
           }
         }
 #pragma unroll
@@ -581,7 +655,12 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       }
       total += (acc[0] + acc[1]) + (acc[2] + acc[3]);   // a tile's sum first: shorter chains of roundings
     }
-    if (ok && j0_64 + r < p.extent) {
+    // the second warpgroup's sums join the first's
+    float *sums = reinterpret_cast<float *>(smem + Cfg::kOffSum);
+    if (x == 1) sums[r] = total;
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (x == 0 && *abort_flag == 0 && j0_64 + r < p.extent) {
+      total += sums[r];
       const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
       float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
       const float gain = j < s.sk ? total : 0.f;
@@ -590,7 +669,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == Cfg::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }

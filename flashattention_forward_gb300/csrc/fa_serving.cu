@@ -466,7 +466,9 @@ fa_status_t weights_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, cons
     L.grid = dim3((unsigned)((cover + p.keys_per_cta - 1) / p.keys_per_cta), (unsigned)Hkv, (unsigned)B);
   } else {
     if ((st = packed_q_map(&L.tm_q, q, (int)group))) return st;
-    L.grid = dim3((unsigned)((cover + 127) / 128), (unsigned)Hkv, (unsigned)B);
+    const int64_t tiles = (cover + 127) / 128;
+    if (tiles > 65535) return fail(FA_ERR_UNSUPPORTED, "more than 65535 key tiles of 128");
+    L.grid = dim3((unsigned)Hkv, (unsigned)B, (unsigned)tiles);
   }
   P.kind = 4;
   P.dk = (int)D;
@@ -495,7 +497,7 @@ fa_status_t evict_build(const fa_tensor_t *weights, fa_tensor_t *weights_out, co
     return fail(FA_ERR_UNSUPPORTED, "(Dk, Dv) = (%lld, %lld) is not compiled", (long long)dk, (long long)dv);
   if ((st = check_scale(k_scale, "k_scale", k_cache, true)) || (st = check_scale(v_scale, "v_scale", v_cache, true))) return st;
   const int64_t B = launch->num_seqs, Hkv = k_cache->shape[2];
-  if (Hkv > 65535) return fail(FA_ERR_UNSUPPORTED, "too many kv heads");
+  if (Hkv > 4096) return fail(FA_ERR_UNSUPPORTED, "too many kv heads");
   if (budget < 1 || sink < 0 || recent < 0 || (int64_t)sink + recent > budget)
     return fail(FA_ERR_INVALID_ARG, "budget %d, sink %d, recent %d: budget >= 1 and sink + recent <= budget", budget, sink, recent);
   if ((st = check_table(block_table, "block_table", B, launch->max_seqlen_k, page_size))) return st;
@@ -666,7 +668,7 @@ int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int
   if (total_q <= 0 || num_groups <= 0 || hkv <= 0 || hq <= 0 || hq % hkv || max_len <= 0) return 1;
   const int64_t tpt = std::max(1, 128 / (hq / hkv));
   const int64_t tiles = std::max<int64_t>((total_q + tpt - 1) / tpt, num_groups) * hkv;
-  const int64_t by_sms = (2 * (int64_t)sm_count() + tiles - 1) / tiles;
+  const int64_t by_sms = 2 * (int64_t)sm_count() / tiles;   // one wave at two CTAs per SM
   const int64_t by_keys = ((int64_t)max_len + 127) / 128;
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(by_sms, by_keys), 64));
 }
