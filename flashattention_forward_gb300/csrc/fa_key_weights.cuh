@@ -21,6 +21,16 @@
 // of its kv head -- (token, head of the group) packed into one tile by a
 // three-dimensional TMA box -- as B.  A thread owns a key, so a column sum is a
 // sum in one register: no shuffles, no atomics, the same result every run.
+//
+// -LSE belongs to a column, i.e. every thread needs all 128 of a tile.  Read
+// from shared memory they cost four cycles per 16 bytes and warp whatever the
+// addresses (the register file takes 128 bytes a cycle), as much as the
+// product's own operands: the kernel was bound by shared memory.  So they ride
+// in the product instead: one more K=16 step adds sum of (parts of 1/k_scale of
+// the key) x (parts of -LSE / scale of the row), each in three bf16 parts, and
+// the exponent's argument is then the accumulator times one factor.  (Not under
+// the soft-cap, which is not linear, nor with ALiBi, which needs the columns'
+// positions in any case.)
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -162,6 +172,44 @@ __global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(c
   const int lo = (int)lo64, hi = (int)min(hi64, (int64_t)sq_.sk);
   kw_carry(p, b, hk, hi, hi64);
 
+  // The first keys are on their way while the query rows are read.
+  const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
+  float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
+  const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
+  // the lane's key rows of a step are base + 8 u + g; their pages are read one step ahead
+  bool bad = false;
+  int pgn[2 * U];
+  auto pages = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < 2 * U; ++u) {
+      const int j = base + 8 * u + g;
+      pgn[u] = kw_page(p, bt, sq_.ka, j, j < hi, bad);
+    }
+  };
+  uint4 kr[2 * U][NP], kn[2 * U][NP];
+  float ks[2 * U], ksn[2 * U];
+  unsigned dead = 0, deadn = 0;               // bit u: the page of key base + 8 u + g is not in the pool
+  auto load = [&](int base) {
+    deadn = 0;
+#pragma unroll
+    for (int u = 0; u < 2 * U; ++u) {
+      const int j = base + 8 * u + g;
+      const bool live = pgn[u] >= 0;
+      const uint8_t *row = kw_row(p, max(pgn[u], 0), j, hk);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) kn[u][i] = live ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
+      ksn[u] = (KV && live) ? kw_scale(p, pgn[u], j, hk) : 1.f;
+      if (!live) deadn |= 1u << u;
+    }
+  };
+  const int step = kKwWarps * 16 * U;
+  int base = lo + warp * 16 * U;
+  pages(base);
+  if (AHEAD) {
+    load(base);
+    pages(base + step);
+  }
+
   // Query rows as B fragments (k16 x n8): row 8 nt + g, the lane's pieces.
   uint32_t qb[D / 16][NT][2];
   float inv[NT];                              // byte caches: 2^-e of row 8 nt + g
@@ -239,42 +287,6 @@ __global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(c
       }
     }
 
-  const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
-  float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
-  const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
-  // the lane's key rows of a step are base + 8 u + g; their pages are read one step ahead
-  bool bad = false;
-  int pgn[2 * U];
-  auto pages = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {
-      const int j = base + 8 * u + g;
-      pgn[u] = kw_page(p, bt, sq_.ka, j, j < hi, bad);
-    }
-  };
-  uint4 kr[2 * U][NP], kn[2 * U][NP];
-  float ks[2 * U], ksn[2 * U];
-  unsigned dead = 0, deadn = 0;               // bit u: the page of key base + 8 u + g is not in the pool
-  auto load = [&](int base) {
-    deadn = 0;
-#pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {
-      const int j = base + 8 * u + g;
-      const bool live = pgn[u] >= 0;
-      const uint8_t *row = kw_row(p, max(pgn[u], 0), j, hk);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) kn[u][i] = live ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
-      ksn[u] = (KV && live) ? kw_scale(p, pgn[u], j, hk) : 1.f;
-      if (!live) deadn |= 1u << u;
-    }
-  };
-  const int step = kKwWarps * 16 * U;
-  int base = lo + warp * 16 * U;
-  pages(base);
-  if (AHEAD) {
-    load(base);
-    pages(base + step);
-  }
   for (; base < hi; base += step) {
     if (!AHEAD) {
       load(base);
@@ -355,9 +367,12 @@ struct KwTileCfg {
   static constexpr int NCH = D == 192 ? 3 : 4;      // Q ring, in blocks; two CTAs per SM
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = KC * kChunkBytes;
-  static constexpr int kOffCol = kOffQ + NCH * kChunkBytes;   // [2][128] -LSE, [2][128] i'
-  static constexpr int kOffSum = kOffCol + 2 * 128 * 8;       // [128] the second warpgroup's sums
-  static constexpr int kOffBar = kOffSum + 128 * 4;
+  static constexpr int kOffCol = kOffQ + NCH * kChunkBytes;   // [2][128] -LSE, [128] tokens
+  static constexpr int kOffSum = kOffCol + 3 * 128 * 4;       // [128] the second warpgroup's sums
+  // K=16 operands of the LSE term, 32-byte swizzled: the keys', and the rows' of two tiles
+  static constexpr int kAugBytes = 128 * 32;
+  static constexpr int kOffAug = kOffSum + 128 * 4;
+  static constexpr int kOffBar = kOffAug + 3 * kAugBytes;
   static constexpr int kSmemBytes = kOffBar + (2 * NCH + 5) * 8 + 16 + 1024;
   // two warpgroups take the tiles in turn, then the producer and the MMA warp
   static constexpr int kThreads = 10 * 32, kFill = 9 * 32;
@@ -381,6 +396,35 @@ __device__ __forceinline__ uint4 kw_bytes8_to_bf16(uint2 w) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// x = h + m + l to about 2^-24 relative, bf16 parts.
+struct Bf16x3 {
+  float h, m, l;
+};
+__device__ __forceinline__ Bf16x3 bf16_parts(float x) {
+  Bf16x3 s;
+  s.h = __bfloat162float(__float2bfloat16_rn(x));
+  s.m = __bfloat162float(__float2bfloat16_rn(x - s.h));
+  s.l = __bfloat162float(__float2bfloat16_rn(x - s.h - s.m));
+  return s;
+}
+// Row r of a K=16 operand: six values, ten zeros; 16-byte chunk c of a row sits
+// at chunk c ^ ((r >> 2) & 1).
+__device__ __forceinline__ void aug_row(uint8_t *base, int r, float v0, float v1, float v2, float v3, float v4, float v5) {
+  uint8_t *row = base + r * 32;
+  const int sw = (r >> 2) & 1;
+  *reinterpret_cast<uint4 *>(row + (sw << 4)) = make_uint4(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3), pack_bf16x2(v4, v5), 0u);
+  *reinterpret_cast<uint4 *>(row + ((1 ^ sw) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// 16 bytes of shared memory, read where it stands (kept out of registers between uses).
+__device__ __forceinline__ int4 kw_lds4(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+// MOD 0: plain scores with a scale that LSE can be divided by; 1: ALiBi (or any
+// scale, with slope 0); 2: soft-cap.
 template <int D, int MOD>
 __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
     fa_key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const KeyWeightsParams p) {
@@ -415,12 +459,13 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
   }
   uint8_t *sK = smem + Cfg::kOffK, *sQ = smem + Cfg::kOffQ;
   float *col_nl = reinterpret_cast<float *>(smem + Cfg::kOffCol);      // [2][128]
-  int *col_ip = reinterpret_cast<int *>(col_nl + 256);                 // [2][128]
+  int *col_tok = reinterpret_cast<int *>(col_nl + 256);                // [128] token of a tile's column
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
   uint64_t *q_empty = q_full + NCH, *s_full = q_empty + NCH, *s_empty = s_full + 2, *k_ready = s_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(k_ready + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int rows_box = tpt * p.group;               // rows of a Q tile, at most 128
+  if (threadIdx.x < 128) col_tok[threadIdx.x] = (int)threadIdx.x < rows_box ? (int)threadIdx.x / p.group : 1 << 20;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NCH; ++i) {
       mbar_init(smem_u32(q_full + i), 1);
@@ -443,6 +488,36 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
+
+  // Thread r of either warpgroup: key j0 + r and its scale (one too small to
+  // divide by is raised to 2^-100, which leaves its products negligible), and
+  // column r of the tiles: token t_lo + it * tpt + r / group, head r % group.
+  const int r = threadIdx.x & 127, j = j0 + r;
+  float key_factor = 1.f;
+  if (p.kv && warp < 8) {
+    bool bad = false;
+    const int pg = kw_page(p, bt, s.ka, j, j < s.sk, bad);
+    if (pg >= 0) key_factor = kw_scale(p, pg, j, hk);
+  }
+  if (MOD == 0 && fabsf(key_factor) < 0x1p-100f) key_factor = 0x1p-100f;
+  const float *lse_r = p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + s.qa;
+  const int ctok = t_lo + r / p.group;
+  // -LSE in log2 units of column r of tile it; -inf for a row that sees nothing
+  auto column_nl = [&](int it) -> float {
+    const int tok = ctok + it * tpt;
+    if (it >= n_tiles || r >= rows_box || tok >= t_hi) return -INFINITY;
+    const float l = __ldg(lse_r + tok);
+    return l == -INFINITY ? -INFINITY : -l * kLog2e;
+  };
+  // Row r of tile it's operand of the LSE term: -LSE / scale.  Rows that see
+  // nothing get a large finite value (0 * inf would be NaN) of the sign that
+  // the scale turns negative.
+  auto write_rows = [&](int it, float nl) {
+    const float v = nl == -INFINITY ? copysignf(0x1p120f, -p.scale_log2) : nl / p.scale_log2;
+    const Bf16x3 q = bf16_parts(v);
+    aug_row(smem + Cfg::kOffAug + (1 + (it & 1)) * Cfg::kAugBytes, r, q.h, q.m, q.h, q.l, q.m, q.h);
+  };
+  auto row_operand = [&](int it) { write_rows(it, column_nl(it)); };
 
   if (warp != Cfg::kProducerWarp) {
     // The key tile as the K-major, 128-byte-swizzled A operand in bf16: any
@@ -494,6 +569,15 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       const int ch = e / ((128 - rows_box) * 8), rest = e % ((128 - rows_box) * 8);
       *reinterpret_cast<uint4 *>(sQ + ch * Cfg::kChunkBytes + rows_box * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
     }
+    if (MOD == 0 && warp < 8) {
+      // LSE term: the keys' operand, and the rows' of the first two tiles
+      const int x = warp >> 2;
+      if (x == 0) {
+        const Bf16x3 a = bf16_parts(1.f / key_factor);
+        aug_row(smem + Cfg::kOffAug, threadIdx.x, a.h, a.h, a.m, a.h, a.m, a.l);
+      }
+      row_operand(x);
+    }
     fence_proxy_async_smem();
     mbar_arrive(smem_u32(k_ready));
   }
@@ -523,6 +607,8 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
       const uint32_t hi = (uint32_t)(dk >> 32), lo_k = (uint32_t)dk;
       const uint32_t lo_q = (uint32_t)smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t aug = smem_desc_sw32(smem_u32(smem + Cfg::kOffAug));
+      const uint32_t aug_lo = (uint32_t)aug, aug_hi = (uint32_t)(aug >> 32);
       int n = 0;
       bool ok = mbar_wait(smem_u32(k_ready), 0, abort_flag, p.err);
       for (int it = 0; ok && it < n_tiles; ++it) {
@@ -544,56 +630,45 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
           tc_commit(smem_u32(q_empty + slot));
         }
         if (!ok) break;
+        if constexpr (MOD == 0)
+          mma_ss_w<1>(d, aug_lo, aug_hi, aug_lo + (uint32_t)((1 + x) * (Cfg::kAugBytes >> 4)), aug_hi, idesc);
         tc_commit(smem_u32(s_full + x));
       }
     }
   } else {
     // --------------------------------------------- one key per thread --
     // Warpgroup x takes the tiles x, x + 2, ...: the tiles of S^T buffer x.
-    const int x = warp >> 2, r = threadIdx.x & 127, j = j0 + r;
+    const int x = warp >> 2;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    float ks = 1.f;
-    if (p.kv) {
-      bool bad = false;
-      const int pg = kw_page(p, bt, s.ka, j, j < s.sk, bad);
-      if (pg >= 0) ks = kw_scale(p, pg, j, hk);
-    }
-    const float c = (MOD == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * ks;
+    const float c = (MOD == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * key_factor;
     const KwVisible vb = kw_visible(p);
-    // column r of a tile: token t_lo + it * tpt + r / group, head r % group
-    const int ctok = t_lo + r / p.group;
-    const float *lse_r = p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + s.qa;
-    float *nl_buf = col_nl + x * 128;
-    int *ip_buf = col_ip + x * 128;                 // i' - j0 + the mask's offset
-    auto column = [&](int it, float &nl, int &ip) {
-      const int tok = ctok + it * tpt;
-      nl = -INFINITY;
-      ip = kKwHidden;
-      if (it < n_tiles && r < rows_box && tok < t_hi) {
-        const float l = __ldg(lse_r + tok);
-        nl = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        ip = tok + s.shift - j0 + vb.add;
-      }
-    };
-    float nl_next;
-    int ip_next;
-    column(x, nl_next, ip_next);
+    float *nl_buf = col_nl + x * 128;               // MOD 1, 2
+    float nl_next = column_nl(MOD == 0 ? x + 2 : x);
     float total = 0.f;
     bool ok = true;
     for (int it = x; it < n_tiles; it += 2) {
-      // this tile's column constants, between the barriers of its readers
-      if (it >= 2) asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-      nl_buf[r] = nl_next;
-      ip_buf[r] = ip_next;
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-      column(it + 2, nl_next, ip_next);
+      if constexpr (MOD != 0) {
+        // this tile's column constants, between the barriers of its readers
+        if (it >= 2) asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+        nl_buf[r] = nl_next;
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+        nl_next = column_nl(it + 2);
+      }
       const int ta = t_lo + it * tpt, tb = min(ta + tpt, t_hi) - 1;    // first and last token of the tile
-      bool mask = tb - ta + 1 < tpt;                 // rows of other sequences may hold anything
+      const int n_tok = tb - ta + 1;
+      bool mask = n_tok < tpt;                       // rows of other sequences may hold anything
       if (p.causal) mask = mask || ta + s.shift < jl;
       if (p.window > 0) mask = mask || tb + s.shift - j0 >= p.window || (!p.causal && jl - ta - s.shift >= p.window);
       ok = mbar_wait(smem_u32(s_full + x), (it >> 1) & 1, abort_flag, p.err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
+      if constexpr (MOD == 0) {
+        // the product has read this buffer's row operand: the next tile's
+        write_rows(it + 2, nl_next);
+        fence_proxy_async_smem();
+        nl_next = column_nl(it + 4);
+      }
+      const int d0 = ta + s.shift - j;               // i' - j of the tile's first token
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -605,7 +680,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
           mbar_arrive(smem_u32(s_empty + x));
         }
         const float4 *nl4 = reinterpret_cast<const float4 *>(nl_buf + q * 32);
-        const int4 *ip4 = reinterpret_cast<const int4 *>(ip_buf + q * 32);
+        const uint32_t tok4 = smem_u32(col_tok + q * 32);
         if constexpr (MOD == 2) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], c);
@@ -621,30 +696,31 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
             fma2v(v[e], v[e + 1], -2.f * p.softcap_log2, n.x + p.softcap_log2, n.y + p.softcap_log2);
             fma2v(v[e + 2], v[e + 3], -2.f * p.softcap_log2, n.z + p.softcap_log2, n.w + p.softcap_log2);
           }
-        } else {
+        } else if constexpr (MOD == 1) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float4 n = nl4[e >> 2];
-            if constexpr (MOD == 1) {
-              const int4 i = ip4[e >> 2];
-              const int o = r + vb.add;              // distance i' - j = i - o
-              n.x = fmaf(-p.alibi_log2, fabsf((float)(i.x - o)), n.x);
-              n.y = fmaf(-p.alibi_log2, fabsf((float)(i.y - o)), n.y);
-              n.z = fmaf(-p.alibi_log2, fabsf((float)(i.z - o)), n.z);
-              n.w = fmaf(-p.alibi_log2, fabsf((float)(i.w - o)), n.w);
-            }
+            const int4 i = kw_lds4(tok4 + 4 * e);
+            n.x = fmaf(-p.alibi_log2, fabsf((float)(i.x + d0)), n.x);
+            n.y = fmaf(-p.alibi_log2, fabsf((float)(i.y + d0)), n.y);
+            n.z = fmaf(-p.alibi_log2, fabsf((float)(i.z + d0)), n.z);
+            n.w = fmaf(-p.alibi_log2, fabsf((float)(i.w + d0)), n.w);
             fma2v(v[e], v[e + 1], c, n.x, n.y);
             fma2v(v[e + 2], v[e + 3], c, n.z, n.w);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) mul2(v[e], v[e + 1], c);
         }
         if (mask) {
+          const int da = d0 + vb.add;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const int4 i = ip4[e >> 2];
-            v[e] = (unsigned)(i.x - r) < vb.range ? v[e] : -INFINITY;
-            v[e + 1] = (unsigned)(i.y - r) < vb.range ? v[e + 1] : -INFINITY;
-            v[e + 2] = (unsigned)(i.z - r) < vb.range ? v[e + 2] : -INFINITY;
-            v[e + 3] = (unsigned)(i.w - r) < vb.range ? v[e + 3] : -INFINITY;
+            const int4 i = kw_lds4(tok4 + 4 * e);
+            v[e] = (i.x < n_tok && (unsigned)(i.x + da) < vb.range) ? v[e] : -INFINITY;
+            v[e + 1] = (i.y < n_tok && (unsigned)(i.y + da) < vb.range) ? v[e + 1] : -INFINITY;
+            v[e + 2] = (i.z < n_tok && (unsigned)(i.z + da) < vb.range) ? v[e + 2] : -INFINITY;
+            v[e + 3] = (i.w < n_tok && (unsigned)(i.w + da) < vb.range) ? v[e + 3] : -INFINITY;
           }
         }
 #pragma unroll

@@ -118,18 +118,6 @@ __device__ __forceinline__ int alibi_side(const PrefillParams &p, const Half &hx
   return 0;
 }
 
-// Shared-memory descriptor of a K-major operand with 32-byte rows (K = 16
-// bf16), 32-byte swizzle (mode 6), 8-row groups 256 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFF) >> 4);
-  d |= (uint64_t)(16 >> 4) << 16;
-  d |= (uint64_t)(256 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)6 << 61;
-  return d;
-}
-
 __device__ __forceinline__ int pair_next(const PrefillParams &p, const PairInfo &pi, int kt) {
   ++kt;
   while (kt < pi.kt_hi && !half_active(p, pi, 0, kt) && !half_active(p, pi, 1, kt)) ++kt;

@@ -462,13 +462,18 @@ fa_status_t weights_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, cons
   const int64_t cover = p.inplace ? std::max<int64_t>(launch->max_seqlen_k, 1) : extent;
   if (rows <= fa::kDecRows) {
     L.row_tiles = rows <= 8 ? 1 : 2;
-    p.keys_per_cta = 512;
+    // Key ranges of about six waves of CTAs (two per SM) if all sequences had
+    // max_seqlen_k keys; ragged batches then make three or so.
+    const int64_t per = B * Hkv * (int64_t)launch->max_seqlen_k / (12 * (int64_t)sm_count());
+    p.keys_per_cta = (int)std::min<int64_t>(4096, std::max<int64_t>(256, (per + 255) / 256 * 256));
     L.grid = dim3((unsigned)((cover + p.keys_per_cta - 1) / p.keys_per_cta), (unsigned)Hkv, (unsigned)B);
   } else {
     if ((st = packed_q_map(&L.tm_q, q, (int)group))) return st;
     const int64_t tiles = (cover + 127) / 128;
     if (tiles > 65535) return fail(FA_ERR_UNSUPPORTED, "more than 65535 key tiles of 128");
     L.grid = dim3((unsigned)Hkv, (unsigned)B, (unsigned)tiles);
+    // the plain tile kernel divides the LSE by the scale
+    if (mod == 0 && !(std::fabs(softmax_scale) >= 0x1p-60f)) p.mod = 1;
   }
   P.kind = 4;
   P.dk = (int)D;

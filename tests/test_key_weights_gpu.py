@@ -197,3 +197,23 @@ def test_lengths_beyond_the_bounds_and_bad_pages_are_flagged():
         out = fa.key_weights(*args, **kw)
         assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
         sl.within(out[1], ref[0][1], ref[1][1])
+
+
+@pytest.mark.parametrize("form", ["rows", "tile"])
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_scales_from_zero_to_large(form, kv):
+    """Key scales of 0 (whatever the bytes), far below and far above the others."""
+    import flashattention_forward_gb300 as fa
+    q_lens, k_lens = ([2], [260]) if form == "rows" else ([200], [260])
+    cache = sl.Cache(k_lens, 2, 64, 64, 16, kv, 5)
+    q = sl.make_q(q_lens[0], 4, 64, 5)
+    f = torch.ones(260, 2)
+    f[::7], f[1::7], f[2::7], f[3::7] = 0.0, 1e-38, 1e-6, 8.0
+    cache.k_scale.view(-1, 2)[cache.rows[0]] *= f
+    opts = dict(causal=True)
+    lse = sl.attention(q, q_lens, cache, k_lens, **opts)[1].float()
+    ref = sl.attention(q, q_lens, cache, k_lens, want="weights", lse=lse, **opts)
+    t = cache.to(DEV)
+    check((q.to(DEV), t["k"], lse.to(DEV), sl.cu(q_lens).to(DEV), t["cu_k"]),
+          dict(max_seqlen_q=q_lens[0], max_seqlen_k=260, block_table=t["bt"], page_size=16, k_scale=t["k_scale"],
+               causal=True), ref)
