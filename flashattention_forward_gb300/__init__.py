@@ -30,7 +30,8 @@ EXPORTED = ("fa_fwd_varlen", "fa_fwd_workspace_bytes", "fa_fwd_default_splits", 
             "fa_last_error", "fa_get_device_error", "fa_version", "fa_fwd_varlen_noalloc",
             "fa_fwd_plan_create", "fa_fwd_plan_launch", "fa_fwd_plan_destroy", "fa_bwd_varlen",
             "fa_bwd_workspace_bytes", "fa_fwd_shared_prefix", "fa_shared_prefix_plan_create",
-            "fa_shared_prefix_workspace_bytes", "fa_shared_prefix_default_splits", "fa_key_weights",
+            "fa_shared_prefix_workspace_bytes", "fa_shared_prefix_default_splits",
+            "fa_shared_prefix_default_own_splits", "fa_key_weights",
             "fa_key_weights_plan_create", "fa_cache_evict")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -169,6 +170,8 @@ def lib() -> ctypes.CDLL:
             L.fa_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
             L.fa_shared_prefix_default_splits.argtypes = [ctypes.c_int64, i32, i32, i32, i32]
             L.fa_shared_prefix_default_splits.restype = i32
+            L.fa_shared_prefix_default_own_splits.argtypes = [i32, i32, ctypes.c_int64, i32]
+            L.fa_shared_prefix_default_own_splits.restype = i32
             L.fa_key_weights.argtypes = [ptr] * 8 + [f32, ptr, f32, i32, i32, P(ScoreMod), i32, P(Launch), ptr]
             L.fa_key_weights.restype = ctypes.c_int
             L.fa_key_weights_plan_create.argtypes = L.fa_key_weights.argtypes[:-1] + [P(ptr)]
@@ -569,6 +572,10 @@ def shared_prefix_default_splits(total_q: int, num_groups: int, max_prefix_len: 
     return int(lib().fa_shared_prefix_default_splits(int(total_q), num_groups, max_prefix_len, hq, hkv))
 
 
+def shared_prefix_default_own_splits(num_seqs: int, max_own_len: int, total_own: int, hkv: int) -> int:
+    return int(lib().fa_shared_prefix_default_own_splits(num_seqs, max_own_len, int(total_own), hkv))
+
+
 def shared_prefix_workspace_bytes(launch: "Launch", prefix: "SharedPrefix", hq: int, dv: int) -> int:
     return int(lib().fa_shared_prefix_workspace_bytes(ctypes.byref(launch), ctypes.byref(prefix), hq, dv))
 
@@ -600,8 +607,7 @@ def _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, *, max_
         prefix_splits = shared_prefix_default_splits(Tq, groups, max_prefix_len, Hq, Hkv)
     if num_splits is None:
         own = max(0, total_k - B * max_prefix_len) if total_k is not None else 0
-        num_splits = max(1, default_splits(B, max_seqlen_q, max(0, max_seqlen_k - max_prefix_len), Hq, Hkv, page_size,
-                                           own))
+        num_splits = shared_prefix_default_own_splits(B, max(0, max_seqlen_k - max_prefix_len), own, Hkv)
     launch = Launch(num_seqs=B, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k, num_splits=num_splits,
                     total_q=Tq, total_k=0)
     prefix = SharedPrefix(cu_groups=cu_groups.data_ptr(), lens=prefix_lens.data_ptr(), num_groups=groups,

@@ -82,30 +82,7 @@ struct DecodeParams {
   float softcap_arg, softcap_log2;    // softmax_scale / cap, cap * log2(e)
   const uint8_t *block_mask;          // [B*Hq, n_qblk, n_kblk] or null
   int32_t n_qblk, n_kblk;
-  // keys behind a shared prefix only (SUFFIX): sequence b starts at the
-  // prefix length of its group
-  const int32_t *cu_groups, *prefix_lens;
-  int32_t num_groups;
-  int64_t max_pages, n_pages;         // entries per block-table row, pages in the pool
 };
-
-// The prefix keys of group g: whole pages, inside the page table.  The suffix
-// pass starts each sequence there, so both use this.
-__device__ __forceinline__ int prefix_keys(const int32_t *prefix_lens, int g, int page_size, int64_t max_pages) {
-  int64_t n = max(0, __ldg(prefix_lens + g));
-  n = min(n, max_pages * page_size);
-  return (int)(n & ~(int64_t)(page_size - 1));
-}
-
-// First index in [lo, hi) whose value exceeds x, of a sorted array.
-__device__ __forceinline__ int upper_bound_i32(const int32_t *a, int lo, int hi, int x) {
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a + mid) <= x) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // DIRECT (byte caches at D = 128, token-major pages): the stage's K and V
 // bytes land 128-byte swizzled and go from shared memory straight into the
@@ -208,11 +185,7 @@ template <int D, int KV, bool V5>
 constexpr bool dec_direct() { return KV != 0 && D == 128 && !V5; }
 
 // R8: every CTA has at most 8 query rows (max_seqlen_q * Hq/Hkv <= 8).
-// SUFFIX: the keys of each sequence from its group's shared prefix on (the
-// prefix is attended by fa_prefix.cuh); a kernel of its own, so that the plain
-// decode keeps its code.  The last split runs to the sequence's end, whatever
-// length the host expected.
-template <int D, int KV = 0, bool V5 = false, bool R8 = false, bool SUFFIX = false>
+template <int D, int KV = 0, bool V5 = false, bool R8 = false>
 __global__ void __launch_bounds__(kDecThreads, (dec_direct<D, KV, V5>() && R8) ? 3 : 2)
     fa_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const DecodeParams p) {
@@ -235,23 +208,11 @@ __global__ void __launch_bounds__(kDecThreads, (dec_direct<D, KV, V5>() && R8) ?
 
   const int split = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int qa = __ldg(p.cu_q + b), sq = __ldg(p.cu_q + b + 1) - qa;
-  int sk = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
-  int rows = sq * p.group;             // <= 16, checked on the host
-  if constexpr (SUFFIX) {
-    // lengths that the host's bounds or the page table do not cover
-    if (rows > kDecRows || sk > p.max_pages * p.page_size) {
-      if (threadIdx.x == 0) record_error(p.err, kErrBounds);
-      rows = min(rows, kDecRows);
-      sk = (int)min((int64_t)sk, p.max_pages * p.page_size);
-    }
-  }
+  const int sk = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  const int rows = sq * p.group;       // <= 16, checked on the host
   if (rows == 0) return;
-  int key_lo = split * p.split_keys;
-  if constexpr (SUFFIX) {
-    const int g = upper_bound_i32(p.cu_groups, 0, p.num_groups + 1, b) - 1;
-    if (g >= 0 && g < p.num_groups) key_lo += prefix_keys(p.prefix_lens, g, p.page_size, p.max_pages);
-  }
-  const int key_hi = (SUFFIX && split == p.num_splits - 1) ? sk : min(sk, key_lo + p.split_keys);
+  const int key_lo = split * p.split_keys;
+  const int key_hi = min(sk, key_lo + p.split_keys);
   // Largest key any row of this CTA may see (causal: the last row's i').
   int vis_hi = key_hi;
   if (p.causal) vis_hi = min(vis_hi, sk);   // last row i' = sk - 1
@@ -360,20 +321,10 @@ __global__ void __launch_bounds__(kDecThreads, (dec_direct<D, KV, V5>() && R8) ?
       const int key0 = key_lo + st * kDecStageKeys + lane * p.rows_per_box;
       return key0 < sk ? __ldg(bt + (key0 >> p.page_shift)) : -1;
     };
-    // SUFFIX: a page outside the pool is flagged and replaced (`none`)
-    auto held = [&](int pg, int none) -> int {
-      if constexpr (SUFFIX) {
-        if (pg < 0 || pg >= p.n_pages) {
-          record_error(p.err, kErrBounds);
-          return none;
-        }
-      }
-      return pg;
-    };
     auto scale_page = [&](int st, int u) -> int {
       if (!KV || !bt || st >= n_stages) return 0;
       const int key = key_lo + st * kDecStageKeys + lane + 32 * u;
-      return key < sk ? held(__ldg(bt + (key >> p.page_shift)), 0) : 0;
+      return key < sk ? __ldg(bt + (key >> p.page_shift)) : 0;
     };
     bool ok = true;
     if (p.gather && bt) {
@@ -385,7 +336,7 @@ __global__ void __launch_bounds__(kDecThreads, (dec_direct<D, KV, V5>() && R8) ?
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int key = key_lo + st * kDecStageKeys + lane + 32 * u;
-          pg[u] = (st < n_stages && key < sk) ? held(__ldg(bt + (key >> p.page_shift)), -1) : -1;
+          pg[u] = (st < n_stages && key < sk) ? __ldg(bt + (key >> p.page_shift)) : -1;
         }
       };
       // one stage in flight: the stage the producer waits for frees once

@@ -11,6 +11,7 @@
 #include "fa_evict.cuh"
 #include "fa_key_weights.cuh"
 #include "fa_prefix.cuh"
+#include "fa_suffix.cuh"
 
 namespace fa {
 
@@ -124,10 +125,20 @@ cudaError_t launch_prefix(int d, const PrefixLaunch &L);
 // Merge of num_splits partials, one warp per (row, head).
 cudaError_t launch_prefix_merge(int d, const float *o_part, const float *lse_part, const int32_t *cu_q, int num_seqs,
                                 int num_splits, int64_t n_rows, int hq, void *out, float *lse, cudaStream_t stream);
-cudaError_t launch_decode_suffix(int d, const DecodeLaunch &L);
+
+// The keys of each sequence behind its group's prefix (fa_suffix.cuh).
+struct SuffixLaunch {
+  CUtensorMap tm_k, tm_v;
+  SuffixParams p;
+  int kv, row_tiles;   // tiles of 8 query rows per sequence and kv head: 1 or 2
+  dim3 grid;
+  cudaStream_t stream;
+};
+cudaError_t launch_suffix(int d, const SuffixLaunch &L);
 
 struct KeyWeightsLaunch {
-  CUtensorMap tm_q;
+  CUtensorMap tm_q;   // tile form
+  CUtensorMap tm_k;   // rows form
   KeyWeightsParams p;
   int row_tiles;   // rows form with this many tiles of 8 rows; 0: tile form
   dim3 grid;
@@ -143,6 +154,23 @@ cudaError_t launch_evict(const EvictLaunch &L);
 
 // Records a host-side error message for fa_last_error() and returns `st`.
 fa_status_t set_host_error(fa_status_t st, const char *msg);
+
+// Launches `kern` so that it may start while the kernel before it on the stream
+// is still running (that one calls pdl_launch(), this one pdl_wait()).
+template <typename... Par, typename... Arg>
+cudaError_t launch_behind(void (*kern)(Par...), dim3 grid, int threads, int smem, cudaStream_t stream, Arg... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 // Sets the dynamic shared-memory attribute once per (kernel, device).
 template <typename K>
@@ -180,7 +208,9 @@ struct fa_fwd_plan_s {
   int64_t rows = 0;
   void *out = nullptr;
   fa::PrefillLaunch pl;
-  fa::PrefixLaunch px;       // kind 3, with dl (the sequences' own keys) and splits (of both passes)
+  fa::PrefixLaunch px;       // kind 3, with sx and the splits of both passes
+  fa::SuffixLaunch sx;
+  float *lse = nullptr;
   fa::KeyWeightsLaunch kw;
   fa::EvictLaunch ev;
 };

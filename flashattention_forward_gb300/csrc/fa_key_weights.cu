@@ -5,11 +5,20 @@
 namespace fa {
 namespace {
 
+template <int D, int KV, int NT>
+cudaError_t rows_one(const KeyWeightsLaunch &L) {
+  static unsigned long long done = 0;
+  auto kern = fa_key_weights_rows_kernel<D, KV, NT>;
+  constexpr int kSmem = KwRowsCfg<D, KV>::kSmemBytes;
+  cudaError_t e = ensure_smem_attr(kern, kSmem, &done);
+  if (e != cudaSuccess) return e;
+  kern<<<L.grid, kKwWarps * 32, kSmem, L.stream>>>(L.tm_k, L.p);
+  return cudaGetLastError();
+}
+
 template <int D, int KV>
 cudaError_t rows_by_tiles(const KeyWeightsLaunch &L) {
-  if (L.row_tiles <= 1) fa_key_weights_rows_kernel<D, KV, 1><<<L.grid, kKwWarps * 32, 0, L.stream>>>(L.p);
-  else fa_key_weights_rows_kernel<D, KV, 2><<<L.grid, kKwWarps * 32, 0, L.stream>>>(L.p);
-  return cudaGetLastError();
+  return L.row_tiles <= 1 ? rows_one<D, KV, 1>(L) : rows_one<D, KV, 2>(L);
 }
 
 template <int D>

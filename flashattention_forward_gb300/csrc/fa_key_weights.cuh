@@ -10,10 +10,8 @@
 //
 // Rows form (few query rows per kv head: decode and drafts).  Bound by
 // reading K once.  The keys go from global memory straight into the A
-// fragments of S^T = K Q^T (mma.sync as a dense FMA engine, as in the split-KV
-// decode): the contraction index is permuted so that a lane's 16-byte piece of
-// a key row is what the lane's fragments hold, hence no shared memory, no
-// barrier, and any page size costs one page-table read per key row.
+// fragments of S^T = K Q^T (fa_rows.cuh): no shared memory, no barrier, and any
+// page size costs one page-table read per key row.
 //
 // Tile form (prompts).  Bound by the QK product and one exponential per pair:
 // S^T tiles of 128 keys x 128 query rows on tcgen05 with fp32 accumulators in
@@ -35,8 +33,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "fa_decode.cuh"
-#include "sm103_ptx.cuh"
+#include "fa_rows.cuh"
 
 namespace fa {
 
@@ -66,6 +63,7 @@ struct KeyWeightsParams {
   int32_t mod, causal, window;
   float scale_log2, alibi_log2, softcap_arg, softcap_log2;
   int32_t keys_per_cta;               // rows form
+  int32_t small_pages;                // rows form: pages of fewer than 16 keys, row copies instead of boxes
   int32_t tokens_per_tile;            // tile form: 128 / group
   int *err;
 };
@@ -114,47 +112,32 @@ __device__ __forceinline__ void kw_carry(const KeyWeightsParams &p, int b, int h
   for (int64_t j = lo + threadIdx.x; j < hi; j += blockDim.x) wo[j] = wi ? p.beta * wi[j] : 0.f;
 }
 
-__device__ __forceinline__ uint4 kw_ld_stream(const uint8_t *a) {
-  uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(a));
-  return v;
-}
-
-// Row i' sees key j iff (unsigned)(i' - j + add) < range, for every mask; a row
-// at kKwHidden sees no key (positions stay below 2^30 in magnitude).
-constexpr int kKwHidden = -(1 << 30) - (1 << 29);
-struct KwVisible {
-  int add;
-  unsigned range;
-};
-__device__ __forceinline__ KwVisible kw_visible(const KeyWeightsParams &p) {
-  KwVisible v;
-  if (p.window > 0) {
-    v.add = p.causal ? 0 : p.window - 1;
-    v.range = p.causal ? (unsigned)p.window : 2u * (unsigned)p.window - 1u;
-  } else {
-    v.add = p.causal ? 0 : 1 << 30;
-    v.range = 1u << 31;
-  }
-  return v;
-}
-
 // --------------------------------------------------------------- rows form --
 constexpr int kKwWarps = 8;
 
+template <int D, int KV>
+struct KwRowsCfg {
+  static constexpr int kRow = D * (KV ? 1 : 2);
+  static constexpr int NP = kRow / 64;                   // 16-byte pieces of a key row per lane
+  // short rows are bound by the work on a group more than by its bytes: more warps
+  static constexpr int kCtasPerSm = kRow <= 128 ? 3 : 2;
+  // as many slots as these CTAs hold, up to six
+  static constexpr int kFit = (222 * 1024 / (kCtasPerSm * kKwWarps) - 1200) / (16 * kRow + 160);
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  using Ring = RowsRing<kRow, 0, KV != 0, kStages>;
+  static constexpr int kSmemBytes = kKwWarps * Ring::kBytes + 1024;
+  static_assert(kStages >= 2 && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
+};
+
 // NT tiles of 8 query rows.
 template <int D, int KV, int NT>
-__global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(const KeyWeightsParams p) {
-  constexpr int ESZ = KV ? 1 : 2;
-  constexpr int NP = D * ESZ / 64;            // 16-byte pieces of a key row per lane
-  // 16-key groups per warp step, 2 to 4 KB of keys.  The next step's are loaded
-  // while this one's are used (AHEAD), so that every warp always has keys in
-  // flight, where two steps' keys and the query fragments fit the registers of
-  // two CTAs per SM.
-  constexpr int U = (NP == 1 ? 4 : (NP == 2 ? 2 : 1)) > NT ? (NP == 1 ? 4 : (NP == 2 ? 2 : 1)) / NT : 1;
-  constexpr bool AHEAD = NP * U <= 4 && NT * D <= 192;
+__global__ void __launch_bounds__(kKwWarps * 32, NT == 1 ? KwRowsCfg<D, KV>::kCtasPerSm : 2)
+    fa_key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const KeyWeightsParams p) {
+  using Cfg = KwRowsCfg<D, KV>;
+  using Ring = typename Cfg::Ring;
+  constexpr int NP = Cfg::NP, S = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hk = blockIdx.y, b = blockIdx.z;
   const KwSeq sq_ = kw_sequence(p, b);
@@ -172,103 +155,47 @@ __global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(c
   const int lo = (int)lo64, hi = (int)min(hi64, (int64_t)sq_.sk);
   kw_carry(p, b, hk, hi, hi64);
 
-  // The first keys are on their way while the query rows are read.
+  // The warp's groups are lo + 16 (warp + 8 i).  Lane l < 16 finds the row of
+  // key base + l; S - 1 groups are under way while one is used, and the first
+  // of them while the query rows are read.
+  constexpr int STEP = kKwWarps * 16;
   const float *wi = p.w_in ? p.w_in + (int64_t)b * p.wi_stride_b + (int64_t)hk * p.wi_stride_h : nullptr;
   float *wo = p.w_out + (int64_t)b * p.wo_stride_b + (int64_t)hk * p.wo_stride_h;
   const int32_t *bt = p.block_table ? p.block_table + (int64_t)b * p.bt_stride : nullptr;
-  // the lane's key rows of a step are base + 8 u + g; their pages are read one step ahead
   bool bad = false;
-  int pgn[2 * U];
-  auto pages = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {
-      const int j = base + 8 * u + g;
-      pgn[u] = kw_page(p, bt, sq_.ka, j, j < hi, bad);
-    }
+  auto page_at = [&](int base) -> int {
+    const int j = base + lane;
+    return kw_page(p, bt, sq_.ka, j, lane < 16 && j < hi, bad);
   };
-  uint4 kr[2 * U][NP], kn[2 * U][NP];
-  float ks[2 * U], ksn[2 * U];
-  unsigned dead = 0, deadn = 0;               // bit u: the page of key base + 8 u + g is not in the pool
-  auto load = [&](int base) {
-    deadn = 0;
-#pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {
-      const int j = base + 8 * u + g;
-      const bool live = pgn[u] >= 0;
-      const uint8_t *row = kw_row(p, max(pgn[u], 0), j, hk);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) kn[u][i] = live ? kw_ld_stream(row + 16 * (t + 4 * i)) : make_uint4(0, 0, 0, 0);
-      ksn[u] = (KV && live) ? kw_scale(p, pgn[u], j, hk) : 1.f;
-      if (!live) deadn |= 1u << u;
-    }
+  const bool small = p.small_pages != 0;
+  Ring ring;
+  ring.init(smem + warp * Ring::kBytes);
+  auto copy = [&](int base, int pg) {
+    const int j = base + lane;
+    const bool live = pg >= 0;
+    ring.start(base < hi, small, &tm_k, nullptr, hk, bt == nullptr, pg, bt ? base & (p.page_size - 1) : sq_.ka + base,
+               live && small ? kw_row(p, pg, j, hk) : nullptr,
+               KV && live ? p.k_scale + ((int64_t)pg * p.page_size + (j & (p.page_size - 1))) * p.hkv + hk : nullptr);
   };
-  const int step = kKwWarps * 16 * U;
-  int base = lo + warp * 16 * U;
-  pages(base);
-  if (AHEAD) {
-    load(base);
-    pages(base + step);
+  const int first = lo + warp * 16;
+  int pgn;
+  {
+    int pg[S - 1];
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) pg[i] = page_at(first + STEP * i);
+    pgn = page_at(first + STEP * (S - 1));
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) copy(first + STEP * i, pg[i]);
   }
 
-  // Query rows as B fragments (k16 x n8): row 8 nt + g, the lane's pieces.
   uint32_t qb[D / 16][NT][2];
   float inv[NT];                              // byte caches: 2^-e of row 8 nt + g
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    const bool live = r < rows;
-    const __nv_bfloat16 *src = p.q;
-    if (live)
-      src = p.q + (int64_t)(sq_.qa + r / p.group) * p.q_stride_t + (int64_t)(hk * p.group + r % p.group) * p.q_stride_h;
-    inv[nt] = 1.f;
-    if constexpr (KV == 0) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const uint4 v = live ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * (t + 4 * i))) : make_uint4(0, 0, 0, 0);
-        qb[2 * i][nt][0] = v.x;
-        qb[2 * i][nt][1] = v.y;
-        qb[2 * i + 1][nt][0] = v.z;
-        qb[2 * i + 1][nt][1] = v.w;
-      }
-    } else {
-      // f16 with a power-of-two factor per row, max|q| 2^e in [2^14, 2^15):
-      // bf16 values within 2^-24 of the row's largest are exact
-      uint4 v[2 * NP];
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          v[2 * i + u] =
-              live ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * i) + 8 * u)) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v[2 * i + u].x, v[2 * i + u].y, v[2 * i + u].z, v[2 * i + u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int sh = 0;
-      if (mx > 0.f && mx <= 3.0e38f) sh = min(141 - (int)((__float_as_uint(mx) >> 23) & 0xFF), 126);
-      const float up = __uint_as_float((uint32_t)(sh + 127) << 23);
-      inv[nt] = __uint_as_float((uint32_t)(127 - sh) << 23);
-#pragma unroll
-      for (int i = 0; i < 2 * NP; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xFFFF0000u) * up);
-        qb[2 * i][nt][0] = h[0];
-        qb[2 * i][nt][1] = h[1];
-        qb[2 * i + 1][nt][0] = h[2];
-        qb[2 * i + 1][nt][1] = h[3];
-      }
-    }
-  }
+  rows_q_fragments<D, KV, NT>(p.q, p.q_stride_t, p.q_stride_h, sq_.qa, hk, p.group, rows, qb, inv);
   // The rows of this lane's C columns, 8 nt + 2t + e: -LSE (log2 units), i'
-  // (relative to key lo + g, with the mask's offset) and the score factor.  Rows that see nothing (LSE -inf) weigh nothing.
-  const KwVisible vb = kw_visible(p);
+  // (relative to key lo + kg, with the mask's offset) and the score factor.
+  // Rows that see nothing (LSE -inf) weigh nothing.
+  const RowsVisible vb = rows_visible(p.causal, p.window);
+  const int kg = Ring::K::row(g);             // the lane's fragment rows: keys kg and kg + 8 of a group
   float nl[NT][2], sc[NT][2];
   int ip[NT][2];
 #pragma unroll
@@ -279,83 +206,76 @@ __global__ void __launch_bounds__(kKwWarps * 32, 2) fa_key_weights_rows_kernel(c
       const float f = __shfl_sync(0xffffffffu, inv[nt], (2 * t + e) * 4);
       sc[nt][e] = (p.mod == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * f;
       nl[nt][e] = -INFINITY;
-      ip[nt][e] = kKwHidden;
+      ip[nt][e] = kRowsHidden;
       if (r < rows) {
         const float l = __ldg(p.lse + (int64_t)(hk * p.group + r % p.group) * p.total_q + sq_.qa + r / p.group);
         nl[nt][e] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-        ip[nt][e] = r / p.group + sq_.shift + vb.add - lo - g;
+        ip[nt][e] = r / p.group + sq_.shift + vb.add - lo - kg;
       }
     }
 
-  for (; base < hi; base += step) {
-    if (!AHEAD) {
-      load(base);
-      pages(base + step);
+  bool ok = true;
+  // the old weights of keys kg and kg + 8, read one group ahead
+  float w0[2] = {0.f, 0.f}, w1[2];
+  auto old_weights = [&](int base, float (&w)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int j = base + 8 * x + kg;
+      w[x] = wi && t == 0 && j < hi ? __ldcs(wi + j) : 0.f;
     }
+  };
+  old_weights(first, w1);
+  for (int base = first; base < hi; base += STEP) {
+    const int ahead = base + STEP * (S - 1);
+    w0[0] = w1[0];
+    w0[1] = w1[1];
+    old_weights(base + STEP, w1);
+    copy(ahead, pgn);
+    pgn = page_at(ahead + STEP);
+    ok = ring.wait(small, p.err);
+    if (!ok) break;
+    const uint32_t st = ring.slot();
+    if (KV || small) __syncwarp();            // what other lanes copied
+    float c[NT][4];
+    {
+      uint4 kr[2][NP];
 #pragma unroll
-    for (int u = 0; u < 2 * U; ++u) {
-      ks[u] = ksn[u];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NP; ++i) kr[u][i] = kn[u][i];
+        for (int i = 0; i < NP; ++i) kr[u][i] = rows_lds16(st + Ring::K::at(t + 4 * i, kg + 8 * u));
+      rows_qk<D, KV, NT>(kr[0], kr[1], qb, c);
     }
-    dead = deadn;
-    if (AHEAD && base + step < hi) {
-      load(base + step);
-      pages(base + 2 * step);
+    float ks[2] = {1.f, 1.f};
+    if constexpr (KV != 0) {
+      ks[0] = rows_lds4(ring.scales() + kg * 4);
+      ks[1] = rows_lds4(ring.scales() + (kg + 8) * 4);
     }
+    ring.next();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float c[NT][4];
+    for (int x = 0; x < 2; ++x) {             // keys base + 8 x + kg
+      const int rel = base - lo + 8 * x, j = lo + rel + kg;
+      float sum = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const uint32_t w0[4] = {kr[2 * u][i].x, kr[2 * u][i].y, kr[2 * u][i].z, kr[2 * u][i].w};
-        const uint32_t w1[4] = {kr[2 * u + 1][i].x, kr[2 * u + 1][i].y, kr[2 * u + 1][i].z, kr[2 * u + 1][i].w};
-        if constexpr (KV == 0) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t a[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(c[nt], a, qb[2 * i + s][nt][0], qb[2 * i + s][nt][1]);
+        for (int e = 0; e < 2; ++e) {
+          const int d = ip[nt][e] - rel;      // i' - j + the mask's offset
+          float y = c[nt][2 * x + e] * (KV ? sc[nt][e] * ks[x] : sc[nt][e]);
+          if (p.mod == 2) {
+            float r;
+            y = softcap_log2_score(ex2(y), p.softcap_log2, r);
+          } else if (p.mod == 1) {
+            y = fmaf(-p.alibi_log2, fabsf((float)(d - vb.add)), y);
           }
-        } else {
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            uint32_t a[4];
-            dec_bytes4_to_f16<KV>(w0[s], a[0], a[2]);
-            dec_bytes4_to_f16<KV>(w1[s], a[1], a[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(c[nt], a, qb[4 * i + s][nt][0], qb[4 * i + s][nt][1]);
-          }
+          y = ex2(y + nl[nt][e]);
+          sum += (unsigned)d < vb.range ? y : 0.f;
         }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {           // keys base + 16 u + 8 x + g
-        const int rel = base - lo + 16 * u + 8 * x, j = lo + rel + g;
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int d = ip[nt][e] - rel;    // i' - j + the mask's offset
-            float y = c[nt][2 * x + e] * (KV ? sc[nt][e] * ks[2 * u + x] : sc[nt][e]);
-            if (p.mod == 2) {
-              float r;
-              y = softcap_log2_score(ex2(y), p.softcap_log2, r);
-            } else if (p.mod == 1) {
-              y = fmaf(-p.alibi_log2, fabsf((float)(d - vb.add)), y);
-            }
-            y = ex2(y + nl[nt][e]);
-            sum += (unsigned)d < vb.range ? y : 0.f;
-          }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (dead & (1u << (2 * u + x))) sum = 0.f;
-        if (t == 0 && j < hi) wo[j] = wi ? fmaf(p.beta, wi[j], sum) : sum;
-      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0 && j < hi) wo[j] = fmaf(p.beta, w0[x], sum);
     }
   }
+  if (!ok) ring.drain();
   if (bad) record_error(p.err, kErrBounds);
 }
 
@@ -535,7 +455,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       for (int i = 0; i < N; ++i) {
         const int e = ft + i * FT, r = e / PR, j = j0 + r;
         const int pg = kw_page(p, bt, s.ka, j, e < 128 * PR && j < s.sk, bad);
-        v[i] = pg >= 0 ? kw_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
+        v[i] = pg >= 0 ? rows_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -549,7 +469,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
       for (int i = 0; i < N; ++i) {
         const int e = ft + i * FT, r = e / PR, j = j0 + r;
         const int pg = kw_page(p, bt, s.ka, j, e < 128 * PR && j < s.sk, bad);
-        v[i] = pg >= 0 ? kw_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
+        v[i] = pg >= 0 ? rows_ld_stream(kw_row(p, pg, j, hk) + (e % PR) * 16) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -641,7 +561,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
     const int x = warp >> 2;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float c = (MOD == 2 ? 2.f * kLog2e * p.softcap_arg : p.scale_log2) * key_factor;
-    const KwVisible vb = kw_visible(p);
+    const RowsVisible vb = rows_visible(p.causal, p.window);
     float *nl_buf = col_nl + x * 128;               // MOD 1, 2
     float nl_next = column_nl(MOD == 0 ? x + 2 : x);
     float total = 0.f;

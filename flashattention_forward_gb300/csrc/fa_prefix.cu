@@ -10,6 +10,14 @@ cudaError_t prefix_one(const PrefixLaunch &L) {
   using Cfg = PrefixCfg<D, KV>;
   static unsigned long long done = 0;
   auto kern = fa_prefix_kernel<D, KV, MOD>;
+  // The softmax warps wait for registers that the others release: the launch
+  // has to hold the whole split (the same for every device of a process).
+  static int fits = -1;
+  if (fits < 0) {
+    cudaFuncAttributes a;
+    fits = cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs * Cfg::kThreads >= Cfg::kPoolNeeded;
+  }
+  if (fits != 1) return cudaErrorNotSupported;
   cudaError_t e = ensure_smem_attr(kern, Cfg::kSmemBytes, &done);
   if (e != cudaSuccess) return e;
   kern<<<L.grid, Cfg::kThreads, Cfg::kSmemBytes, L.stream>>>(L.tm_q, L.tm_k, L.tm_v, L.p);
@@ -40,6 +48,7 @@ __global__ void __launch_bounds__(128) fa_prefix_merge_kernel(const float *__res
                                                               const int32_t *__restrict__ cu_q, int num_seqs,
                                                               int num_splits, int64_t n_rows, int hq,
                                                               __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+  pdl_wait();
   const int64_t wid = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (wid >= n_rows * hq) return;
@@ -107,8 +116,8 @@ cudaError_t launch_prefix_merge(int d, const float *o_part, const float *lse_par
   const unsigned blocks = (unsigned)((n_rows * hq * 32 + threads - 1) / threads);
   auto *o = reinterpret_cast<__nv_bfloat16 *>(out);
   auto kern = d == 64 ? fa_prefix_merge_kernel<64> : fa_prefix_merge_kernel<128>;
-  kern<<<blocks, threads, 0, stream>>>(o_part, lse_part, cu_q, num_seqs, num_splits, n_rows, hq, o, lse);
-  return cudaGetLastError();
+  return launch_behind(kern, dim3(blocks), threads, 0, stream, o_part, lse_part, cu_q, num_seqs, num_splits, n_rows, hq, o,
+                       lse);
 }
 
 }  // namespace fa

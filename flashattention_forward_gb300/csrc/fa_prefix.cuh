@@ -22,7 +22,7 @@
 // causal limit and window), so the result does not depend on the prefix lying
 // left of all queries; key tiles that no row sees are not loaded.
 //
-// Byte caches (KV 1 e4m3, 2 int8): two converter warps turn the staged bytes
+// Byte caches (KV 1 e4m3, 2 int8): six converter warps turn the staged bytes
 // into f16 (exact) in place; k_scale multiplies the scores and v_scale the
 // weights in fp32.  The reference of the exponentials includes the tile's
 // largest v_scale, so that the scaled weights use f16's range whatever the
@@ -30,8 +30,8 @@
 #pragma once
 #include <climits>
 
-#include "fa_decode.cuh"
 #include "fa_prefill.cuh"
+#include "fa_suffix.cuh"
 
 namespace fa {
 
@@ -74,8 +74,14 @@ struct PrefixCfg {
   static constexpr int kNumBars = 2 + 6 * NS + 3 + NSS;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
-  static constexpr int kThreads = 8 * 32;
+  // warps: 0-3 softmax, 4 producer, 5 MMA, then the converters (bf16: two idle
+  // warps that fill the warpgroup); the softmax warps take registers from the
+  // others (setmaxnreg), within what the launch holds at two CTAs per SM
+  static constexpr int kThreads = (KV ? 12 : 8) * 32, kConverters = 6;
+  static constexpr int kRegsSoftmax = KV ? 144 : 200, kRegsOther = KV ? 48 : 56;
+  static constexpr int kPoolNeeded = 128 * kRegsSoftmax + (kThreads - 128) * kRegsOther;
   static constexpr uint32_t kTmemCols = 256;           // S (and P) [0,128), O [128, 128 + D)
+  static_assert(2 * kPoolNeeded <= 65536, "two CTAs per SM");
   static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
 };
 
@@ -86,13 +92,6 @@ __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// 32 bytes, one sector.
-__device__ __forceinline__ void st_global_f8(float *dst, const float *v) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
 }
 
 // MOD: 0 plain with a positive scale, 1 ALiBi (or any scale), 2 soft-cap.
@@ -106,6 +105,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, hk = blockIdx.y;
+  pdl_launch();   // the sequences' own keys need nothing of this pass
 
   // ------------------------------------------------------------ work tile --
   // The tiles of all groups in a row; every warp finds this one's group.
@@ -184,9 +184,16 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   int row_lo = 0, row_hi = INT_MAX, ip = 0;
   if (threadIdx.x < 128) {
     const int r = threadIdx.x;
+    // the row's sequence: the last that starts at or before its token, counted
+    // by the warp 32 sequences at a time
+    const int tok = tok0 + min(r, rows - 1) / p.group;
+    int b = s0 - 1;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const int start = i0 + lane < s1 ? __ldg(p.cu_q + i0 + lane) : INT_MAX;
+#pragma unroll 8
+      for (int k = 0; k < 32; ++k) b += __shfl_sync(0xffffffffu, start, k) <= tok;
+    }
     if (r < rows) {
-      const int tok = tok0 + r / p.group;
-      const int b = upper_bound_i32(p.cu_q, s0, s1, tok) - 1;
       const int qa = __ldg(p.cu_q + b), sq = __ldg(p.cu_q + b + 1) - qa;
       const int sk = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
       ip = tok - qa + sk - sq;
@@ -242,6 +249,8 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     }
     return pg;
   };
+
+  if (warp >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
 
   if (warp == 4) {
     // ------------------------------------------------ producer: Q, K, V --
@@ -395,19 +404,19 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     }
   } else if (warp >= 6) {
     // ---------------------------------------- converters (byte caches) --
-    // Slices of 32 rows x 64 columns, K's then V's of a tile, alternate
-    // between the two warps.  A slice's bytes lie in the upper half of its own
+    // Slices of 32 rows x 64 columns, K's then V's of a tile, in turn to the
+    // six warps.  A slice's bytes lie in the upper half of its own
     // f16 output: step t writes rows 8t..8t+7, whose 1 KB overlaps only
     // staging rows that earlier steps (or this step, before its writes) read.
     if constexpr (KV != 0) {
       const int cw = warp - 6;
-      // warp 6 brings the K scales of a tile, warp 7 the V scales, one tile ahead
-      const float *sc_src = cw ? p.v_scale : p.k_scale;
+      // the first two warps bring the K and the V scales of a tile, one tile ahead
+      const float *sc_src = cw == 1 ? p.v_scale : p.k_scale;
       auto scales = [&](int kt, float (&s)[4]) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           s[u] = 0.f;
-          if (kt >= kt_hi) continue;
+          if (cw > 1 || kt >= kt_hi) continue;
           const int key = kt * kBlockN + lane + 32 * u;
           const int pg = page_of(key);
           if (pg >= 0) s[u] = __ldg(sc_src + ((int64_t)pg * p.page_size + (key & (p.page_size - 1))) * p.hkv + hk);
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t *tile_base = (half ? sV : sK) + st * Cfg::kTileBytes;
-          for (int sl = cw; sl < 4 * KC; sl += 2) {
+          for (int sl = (cw + (half ? 4 * KC : 0)) % Cfg::kConverters; sl < 4 * KC; sl += Cfg::kConverters) {
             uint8_t *base = tile_base + (sl >> 2) * Cfg::kChunkBytes + (sl & 3) * 4096;
             const uint8_t *stg = base + 2048;
 #pragma unroll
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(full + st));
           }
-          if (half == 0) {
+          if (half == 0 && cw < 2) {
             float *dst = sSc + (j % Cfg::NSS) * 256 + cw * 128;
 #pragma unroll
             for (int u = 0; u < 4; ++u) dst[lane + 32 * u] = sc[u];
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     }
   } else {
     // ---------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsSoftmax));
     const int r = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const uint32_t sa = tmem + lane_base, oa = tmem + lane_base + 128;

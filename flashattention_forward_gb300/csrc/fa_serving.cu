@@ -155,6 +155,27 @@ fa_status_t packed_q_map(CUtensorMap *m, const fa_tensor_t *q, int group) {
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, "q");
 }
 
+// TMA map over a token-major cache for the ring of fa_rows.cuh: boxes of 16 keys
+// of one kv head, one block of 128 or 64 bytes wide.
+fa_status_t rows_map(CUtensorMap *m, const fa_tensor_t *t, bool paged, const char *what) {
+  const int esz = dtype_size(t->dtype), nd = paged ? 4 : 3;
+  const int64_t d = t->shape[nd - 1], row = d * esz;
+  const bool sw = row % 128 == 0;
+  uint64_t dims[4], str[3];
+  uint32_t box[4] = {(uint32_t)((sw ? 128 : 64) / esz), 1, 16, 1};
+  dims[0] = (uint64_t)d;
+  dims[1] = (uint64_t)t->shape[nd - 2];
+  dims[2] = (uint64_t)t->shape[nd - 3];
+  str[0] = (uint64_t)(t->stride[nd - 2] * esz);
+  str[1] = (uint64_t)(t->stride[nd - 3] * esz);
+  if (paged) {
+    dims[3] = (uint64_t)t->shape[0];
+    str[2] = (uint64_t)(t->stride[0] * esz);
+  }
+  return make_map(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd, t->data, dims, str, box,
+                  what, sw ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 int32_t clamp_window(int32_t window) { return window <= 0 ? 0 : (int32_t)std::min<int64_t>(window, kMaxLen); }
 
 int kv_code(int dtype) { return dtype == FA_E4M3 ? 1 : (dtype == FA_I8 ? 2 : 0); }
@@ -242,7 +263,8 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
     const uint32_t box[4] = {cols, 1, (uint32_t)rows, 1};
     return make_map(m, kv ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims, str, box, what, swz);
   };
-  const bool gather = page_size < 16;
+  // (an empty pool has no map: its pages are all out of range, and rows become zeros)
+  const bool gather = page_size < 16 || n_pages == 0;
   // ---- the prefix pass
   fa::PrefixLaunch &X = P.px;
   memset(&X, 0, sizeof X);
@@ -294,59 +316,59 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   X.mod = (mod == 0 && !(softmax_scale > 0.f)) ? 1 : mod;
   X.grid = dim3((unsigned)Sp, (unsigned)Hkv, (unsigned)tiles);
   // ---- the sequences' own keys
-  fa::DecodeLaunch &L = P.dl;
+  fa::SuffixLaunch &L = P.sx;
   memset(&L, 0, sizeof L);
-  L.kv = kv;
-  L.rows8 = (int64_t)launch->max_seqlen_q * group <= 8;
-  const int rows_d = std::min(page_size, fa::kDecStageKeys);
-  if (n_pages > 0) {
-    const CUtensorMapSwizzle swz = (!kv || D == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    const uint32_t cols = kv ? (uint32_t)D : 64;
-    if ((st = cache_map(&L.tm_k, k_cache, cols, rows_d, swz, "k")) || (st = cache_map(&L.tm_v, v_cache, cols, rows_d, swz, "v")))
-      return st;
-  }
-  fa::DecodeParams &d = L.p;
+  fa::SuffixParams &d = L.p;
   d.q = (const __nv_bfloat16 *)q->data;
   d.q_stride_t = q->stride[0];
   d.q_stride_h = q->stride[1];
   d.cu_q = p.cu_q;
   d.cu_k = p.cu_k;
+  d.cu_groups = p.cu_groups;
+  d.prefix_lens = p.prefix_lens;
+  d.num_groups = p.num_groups;
   d.block_table = p.block_table;
   d.bt_stride = p.bt_stride;
+  d.max_pages = p.max_pages;
+  d.n_pages = n_pages;
   d.page_size = page_size;
   d.page_shift = p.page_shift;
-  d.rows_per_box = rows_d;
-  d.boxes_per_stage = fa::kDecStageKeys / rows_d;
-  d.gather = gather;
-  d.gk = p.gk;
-  d.gv = p.gv;
-  d.pro_vmul = 1.f;
-  d.mod = mod;
-  d.alibi_log2 = p.alibi_log2;
-  d.softcap_arg = p.softcap_arg;
-  d.softcap_log2 = p.softcap_log2;
+  d.small_pages = gather;
+  if (!gather && ((st = rows_map(&L.tm_k, k_cache, true, "k rows")) || (st = rows_map(&L.tm_v, v_cache, true, "v rows"))))
+    return st;
+  d.k = (const uint8_t *)k_cache->data;
+  d.v = (const uint8_t *)v_cache->data;
+  d.k_page = k_cache->stride[0] * esz;
+  d.k_slot = k_cache->stride[1] * esz;
+  d.k_head = k_cache->stride[2] * esz;
+  d.v_page = v_cache->stride[0] * esz;
+  d.v_slot = v_cache->stride[1] * esz;
+  d.v_head = v_cache->stride[2] * esz;
+  d.k_scale = p.k_scale;
+  d.v_scale = p.v_scale;
+  d.num_seqs = (int)B;
   d.hq = p.hq;
   d.hkv = p.hkv;
   d.group = group;
   const int64_t own_keys = std::max<int64_t>(launch->max_seqlen_k - (int64_t)prefix->max_len, 1);
-  const int64_t per = (own_keys + Ss - 1) / Ss;
-  d.split_keys = (int)((per + fa::kDecStageKeys - 1) / fa::kDecStageKeys * fa::kDecStageKeys);
+  d.split_keys = (int)(((own_keys + Ss - 1) / Ss + 15) / 16 * 16);
   d.num_splits = Ss;
-  d.causal = p.causal;
-  d.window = window;
-  d.total_q = Tq;
-  d.scale_log2 = p.scale_log2;
   d.o_part = o_part + (int64_t)Sp * Tq * Hq * D;
   d.lse_part = lse_part + (int64_t)Sp * Hq * Tq;
+  d.total_q = Tq;
+  d.mod = mod;
+  d.causal = p.causal;
+  d.window = window;
+  d.scale_log2 = p.scale_log2;
+  d.alibi_log2 = p.alibi_log2;
+  d.softcap_arg = p.softcap_arg;
+  d.softcap_log2 = p.softcap_log2;
   d.err = p.err;
-  d.k_scale = p.k_scale;
-  d.v_scale = p.v_scale;
-  d.cu_groups = p.cu_groups;
-  d.prefix_lens = p.prefix_lens;
-  d.num_groups = p.num_groups;
-  d.max_pages = p.max_pages;
-  d.n_pages = n_pages;
-  L.grid = dim3((unsigned)Ss, (unsigned)Hkv, (unsigned)B);
+  L.kv = kv;
+  L.row_tiles = (int64_t)launch->max_seqlen_q * group <= 8 ? 1 : 2;
+  const int64_t units = (int64_t)Ss * Hkv * B;
+  if (units >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "too many key ranges (splits * kv heads * sequences)");
+  L.grid = dim3((unsigned)((units + fa::kSufWarps - 1) / fa::kSufWarps));
   P.kind = 3;
   P.dk = D_;
   P.splits = S;
@@ -354,7 +376,7 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   P.hq = (int)Hq;
   P.dv = D_;
   P.out = out->data;
-  d.lse = lse ? (float *)lse->data : nullptr;   // written by the merge
+  P.lse = lse ? (float *)lse->data : nullptr;
   return FA_OK;
 }
 
@@ -462,9 +484,11 @@ fa_status_t weights_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, cons
   const int64_t cover = p.inplace ? std::max<int64_t>(launch->max_seqlen_k, 1) : extent;
   if (rows <= fa::kDecRows) {
     L.row_tiles = rows <= 8 ? 1 : 2;
-    // Key ranges of about six waves of CTAs (two per SM) if all sequences had
-    // max_seqlen_k keys; ragged batches then make three or so.
-    const int64_t per = B * Hkv * (int64_t)launch->max_seqlen_k / (12 * (int64_t)sm_count());
+    p.small_pages = (paged && page_size < 16) || p.n_pages == 0;
+    if (!p.small_pages && (st = rows_map(&L.tm_k, k_cache, paged, "k rows"))) return st;
+    // Key ranges of about twelve waves of CTAs (two per SM) if all sequences
+    // had max_seqlen_k keys; ragged batches then make six or so.
+    const int64_t per = B * Hkv * (int64_t)launch->max_seqlen_k / (24 * (int64_t)sm_count());
     p.keys_per_cta = (int)std::min<int64_t>(4096, std::max<int64_t>(256, (per + 255) / 256 * 256));
     L.grid = dim3((unsigned)((cover + p.keys_per_cta - 1) / p.keys_per_cta), (unsigned)Hkv, (unsigned)B);
   } else {
@@ -624,14 +648,14 @@ fa_status_t enqueue(const fa_fwd_plan_s &P, cudaStream_t s) {
     e = fa::launch_prefix(P.dk, X);
     what = "prefix launch";
     if (e == cudaSuccess) {
-      fa::DecodeLaunch L = P.dl;
+      fa::SuffixLaunch L = P.sx;
       L.stream = s;
-      e = fa::launch_decode_suffix(P.dk, L);
-      what = "decode launch";
+      e = fa::launch_suffix(P.dk, L);
+      what = "suffix launch";
     }
     if (e == cudaSuccess) {
       e = fa::launch_prefix_merge(P.dk, P.px.p.o_part, P.px.p.lse_part, P.px.p.cu_q, P.px.p.num_seqs, P.splits, P.rows,
-                                  P.hq, P.out, P.dl.p.lse, s);
+                                  P.hq, P.out, P.lse, s);
       what = "merge launch";
     }
   } else if (P.kind == 4) {
@@ -676,6 +700,17 @@ int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int
   const int64_t by_sms = 2 * (int64_t)sm_count() / tiles;   // one wave at two CTAs per SM
   const int64_t by_keys = ((int64_t)max_len + 127) / 128;
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(by_sms, by_keys), 64));
+}
+
+int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max_own_len, int64_t total_own, int32_t hkv) {
+  if (num_seqs <= 0 || hkv <= 0 || max_own_len <= 0) return 1;
+  // Ranges that make about two waves of the decode's warps (12 per SM), 64 to
+  // 1024 keys each: short ones balance ragged batches, long ones write fewer
+  // partials.
+  const double total = total_own > 0 ? (double)total_own : 0.5 * max_own_len * num_seqs;
+  double per = total * hkv / (24.0 * sm_count());
+  per = std::min(1024.0, std::max(64.0, per));
+  return (int32_t)std::min<int64_t>(1024, std::max<int64_t>(1, (int64_t)std::ceil(max_own_len / per)));
 }
 
 fa_status_t fa_fwd_shared_prefix(const fa_tensor_t *q, const fa_tensor_t *k_cache, const fa_tensor_t *v_cache,

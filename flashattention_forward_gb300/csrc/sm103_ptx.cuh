@@ -345,6 +345,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Programmatic dependent launch: the kernel launched behind this one with the
+// attribute may start once every CTA has called pdl_launch() or ended; it waits
+// for this one's completion and memory with pdl_wait().
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ int elect_lane0() { return (threadIdx.x & 31) == 0; }
 
 }  // namespace fa

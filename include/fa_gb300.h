@@ -405,7 +405,7 @@ FA_API fa_status_t fa_fwd_varlen_noalloc(const fa_tensor_t *q, const fa_tensor_t
  * prefix is still attended in full), num_splits >= 1 cuts each prefix into
  * that many key ranges (fa_shared_prefix_default_splits).  launch->num_splits
  * >= 1 cuts the keys behind the prefix likewise, sized by max_seqlen_k -
- * max_len.
+ * max_len (fa_shared_prefix_default_own_splits).
  */
 typedef struct {
     const int32_t *cu_groups;   /* device, int32 [num_groups + 1] */
@@ -427,8 +427,7 @@ typedef struct {
  * Three kernels: the prefix pass, the sequences' own keys, the merge.
  * FA_ERR_UNSUPPORTED for packed K/V, the 5-D pages, other head dims or more
  * query rows; other errors as fa_fwd_varlen.  A page id outside the pool
- * counts as a page of zeros; where the prefix pass meets it, it records
- * FA_ERR_DEVICE_BOUNDS.
+ * counts as a page of zeros and records FA_ERR_DEVICE_BOUNDS.
  */
 FA_API fa_status_t fa_fwd_shared_prefix(const fa_tensor_t *q, const fa_tensor_t *k_cache, const fa_tensor_t *v_cache,
                                  const fa_tensor_t *block_table, const fa_tensor_t *cu_seqlens_q,
@@ -455,9 +454,12 @@ FA_API fa_status_t fa_shared_prefix_plan_create(const fa_tensor_t *q, const fa_t
 FA_API size_t fa_shared_prefix_workspace_bytes(const fa_launch_t *launch, const fa_shared_prefix_t *prefix, int32_t hq,
                                         int32_t dv);
 
-/* Recommended number of key ranges of the prefix pass (>= 1). */
+/* Recommended number of key ranges of the prefix pass, and of the pass over
+ * the keys behind it (max_own_len: the longest sequence's such keys; total_own:
+ * their sum over the sequences, 0 if unknown).  Both are >= 1. */
 FA_API int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq,
                                         int32_t hkv);
+FA_API int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max_own_len, int64_t total_own, int32_t hkv);
 
 /*
  * fa_key_weights -- the attention weight that each key received, summed over
@@ -484,7 +486,8 @@ FA_API int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_grou
  *  launch       num_seqs, max_seqlen_q, max_seqlen_k, total_q (and total_k
  *               for packed K); no workspace.  max_seqlen_k and max_seqlen_q
  *               bound the lengths: a longer sequence records
- *               FA_ERR_DEVICE_BOUNDS and its excess is left out.
+ *               FA_ERR_DEVICE_BOUNDS and its excess is left out.  A page id
+ *               outside the pool counts as keys of zeros and records it too.
  * One kernel: for max_seqlen_q * Hq/Hkv <= 16 bound by reading K, otherwise
  * tensor-core tiles.  Sums are fp32 in a fixed order (the same bits each run).
  */

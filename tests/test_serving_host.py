@@ -140,6 +140,10 @@ def test_shared_prefix_sizes(L):
     assert fa.shared_prefix_default_splits(64, 1, 0, 32, 8) == 1
     assert 1 <= fa.shared_prefix_default_splits(64, 1, 8192, 32, 8) <= 64
     assert fa.shared_prefix_default_splits(1 << 20, 1, 8192, 32, 8) == 1
+    assert fa.shared_prefix_default_own_splits(4, 0, 0, 8) == 1
+    assert fa.shared_prefix_default_own_splits(4, 64, 256, 8) == 1
+    assert fa.shared_prefix_default_own_splits(4, 65, 256, 8) == 2
+    assert 2 <= fa.shared_prefix_default_own_splits(64, 8192, 64 * 4000, 8) <= 64
 
 
 def call_weights(L, plan=False, **over):
