@@ -168,7 +168,7 @@ def lib() -> ctypes.CDLL:
             L.fa_shared_prefix_plan_create.restype = ctypes.c_int
             L.fa_shared_prefix_workspace_bytes.argtypes = [P(Launch), P(SharedPrefix), i32, i32]
             L.fa_shared_prefix_workspace_bytes.restype = ctypes.c_size_t
-            L.fa_shared_prefix_default_splits.argtypes = [ctypes.c_int64, i32, i32, i32, i32]
+            L.fa_shared_prefix_default_splits.argtypes = [ctypes.c_int64, i32, i32, i32, i32, i32]
             L.fa_shared_prefix_default_splits.restype = i32
             L.fa_shared_prefix_default_own_splits.argtypes = [i32, i32, ctypes.c_int64, i32]
             L.fa_shared_prefix_default_own_splits.restype = i32
@@ -568,8 +568,9 @@ class _Prepared:
             self._plan = None
 
 
-def shared_prefix_default_splits(total_q: int, num_groups: int, max_prefix_len: int, hq: int, hkv: int) -> int:
-    return int(lib().fa_shared_prefix_default_splits(int(total_q), num_groups, max_prefix_len, hq, hkv))
+def shared_prefix_default_splits(total_q: int, num_groups: int, max_prefix_len: int, hq: int, hkv: int,
+                                 kv_dtype: int = FA_BF16) -> int:
+    return int(lib().fa_shared_prefix_default_splits(int(total_q), num_groups, max_prefix_len, hq, hkv, kv_dtype))
 
 
 def shared_prefix_default_own_splits(num_seqs: int, max_own_len: int, total_own: int, hkv: int) -> int:
@@ -604,7 +605,7 @@ def _shared_prefix_args(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, *, max_
         softmax_scale = 1.0 / math.sqrt(D)
     groups = cu_groups.shape[0] - 1
     if prefix_splits is None:
-        prefix_splits = shared_prefix_default_splits(Tq, groups, max_prefix_len, Hq, Hkv)
+        prefix_splits = shared_prefix_default_splits(Tq, groups, max_prefix_len, Hq, Hkv, kv_dt)
     if num_splits is None:
         own = max(0, total_k - B * max_prefix_len) if total_k is not None else 0
         num_splits = shared_prefix_default_own_splits(B, max(0, max_seqlen_k - max_prefix_len), own, Hkv)

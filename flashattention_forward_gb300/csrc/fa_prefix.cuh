@@ -11,19 +11,22 @@
 // sequence's own keys by the split-KV rule
 //   LSE = ln sum_s exp(LSE_s),  out = sum_s exp(LSE_s - LSE) O_s.
 //
-// CTA (key split, kv head, tile of 128 rows): S = Q K^T and O += P V on tcgen05
-// with S, P and O in TMEM.  A TMA box of {64 columns, Hq/Hkv heads, 128 /
-// (Hq/Hkv) tokens} lands Q with the heads of a kv head beside each other, so a
-// GQA group fills the tile's rows and K/V are read once for all its heads.  One
-// tile per CTA and two CTAs per SM: one CTA's softmax runs under the other's
-// products, and 64 KB of K and V are in flight per CTA.
+// CTA (key split, kv head, rows): S = Q K^T and O += P V on tcgen05 with S, P
+// and O in TMEM.  A TMA box of {64 columns, Hq/Hkv heads, 128 / (Hq/Hkv)
+// tokens} lands Q with the heads of a kv head beside each other, so a GQA group
+// fills a tile's 128 rows and K/V are read once for all its heads.
+//
+// bf16 caches: one tile per CTA and two CTAs per SM, so that one CTA's softmax
+// runs under the other's products; 64 KB of K and V are in flight per CTA.
 //
 // Every row has its own interval of visible keys (its sequence's length,
 // causal limit and window), so the result does not depend on the prefix lying
 // left of all queries; key tiles that no row sees are not loaded.
 //
-// Byte caches (KV 1 e4m3, 2 int8): six converter warps turn the staged bytes
-// into f16 (exact) in place; k_scale multiplies the scores and v_scale the
+// Byte caches (KV 1 e4m3, 2 int8): two tiles A and B per CTA, each with its
+// softmax warpgroup, share every K/V tile, which halves the conversion per
+// product:  QK_A(0) QK_B(0) | PV_A(0) QK_A(1) PV_B(0) QK_B(1) | ...  Six
+// converter warps turn the staged bytes into f16 (exact) in place; k_scale multiplies the scores and v_scale the
 // weights in fp32.  The reference of the exponentials includes the tile's
 // largest v_scale, so that the scaled weights use f16's range whatever the
 // magnitude of V.
@@ -58,31 +61,34 @@ struct PrefixParams {
 
 template <int D, int KV>
 struct PrefixCfg {
+  static constexpr int NT = KV ? 2 : 1;                // row tiles per CTA
   static constexpr int KC = D / 64;
   static constexpr int kChunkBytes = 128 * 128;        // one 64-column block of 128 rows, 16-bit
   static constexpr int kTileBytes = KC * kChunkBytes;
-  static constexpr int NS = D == 64 ? 2 : 1;           // K and V stages
+  static constexpr int NS = (D == 64 ? 2 : 1) * NT;    // K and V stages
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTileBytes;
+  static constexpr int kOffK = NT * kTileBytes;
   static constexpr int kOffV = kOffK + NS * kTileBytes;
   // byte caches: scales of NSS tiles, [128 of K, 128 of V] each.  Tile j's take
-  // the slot of tile j - NS - 1: its K bytes landed after QK(j - NS), which was
-  // issued after the softmax of tile j - NS - 1.
+  // the slot of tile j - NS - 1: its K bytes landed after the QKs of tile
+  // j - NS, which were issued after the softmax of tile j - NS - 1.
   static constexpr int NSS = NS + 1;
   static constexpr int kOffSc = kOffV + NS * kTileBytes;
   static constexpr int kOffBar = kOffSc + (KV ? NSS * 256 * 4 : 0);
-  static constexpr int kNumBars = 2 + 6 * NS + 3 + NSS;
+  static constexpr int kNumBars = 1 + NT + 6 * NS + 3 * NT + NSS;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
-  // warps: 0-3 softmax, 4 producer, 5 MMA, then the converters (bf16: two idle
-  // warps that fill the warpgroup); the softmax warps take registers from the
-  // others (setmaxnreg), within what the launch holds at two CTAs per SM
-  static constexpr int kThreads = (KV ? 12 : 8) * 32, kConverters = 6;
-  static constexpr int kRegsSoftmax = KV ? 144 : 200, kRegsOther = KV ? 48 : 56;
-  static constexpr int kPoolNeeded = 128 * kRegsSoftmax + (kThreads - 128) * kRegsOther;
-  static constexpr uint32_t kTmemCols = 256;           // S (and P) [0,128), O [128, 128 + D)
-  static_assert(2 * kPoolNeeded <= 65536, "two CTAs per SM");
-  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+  // warps: NT softmax warpgroups, producer, MMA, then the converters (bf16: two
+  // idle warps that fill the warpgroup); the softmax warps take registers from
+  // the others (setmaxnreg), within what the launch holds
+  static constexpr int kCtasPerSm = KV ? 1 : 2;
+  static constexpr int kThreads = (KV ? 16 : 8) * 32, kConverters = 6;
+  static constexpr int kProducerWarp = 4 * NT, kMmaWarp = 4 * NT + 1, kFirstConverter = 4 * NT + 2;
+  static constexpr int kRegsSoftmax = KV ? 152 : 200, kRegsOther = KV ? 104 : 56;
+  static constexpr int kPoolNeeded = NT * 128 * kRegsSoftmax + (kThreads - NT * 128) * kRegsOther;
+  static constexpr uint32_t kTmemCols = NT * 256;      // S (and P) of each tile, then O of each
+  static_assert(kCtasPerSm * kPoolNeeded <= 65536, "register file");
+  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
 };
 
 __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t *r) {
@@ -96,11 +102,11 @@ __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t 
 
 // MOD: 0 plain with a positive scale, 1 ALiBi (or any scale), 2 soft-cap.
 template <int D, int KV, int MOD>
-__global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
+__global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::kCtasPerSm)
     fa_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
   using Cfg = PrefixCfg<D, KV>;
-  constexpr int KC = Cfg::KC, NS = Cfg::NS;
+  constexpr int KC = Cfg::KC, NS = Cfg::NS, NT = Cfg::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -108,7 +114,8 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   pdl_launch();   // the sequences' own keys need nothing of this pass
 
   // ------------------------------------------------------------ work tile --
-  // The tiles of all groups in a row; every warp finds this one's group.
+  // The CTAs' rows (NT tiles) of all groups in a row; every warp finds this one's group.
+  const int tokens = NT * p.tokens_per_tile;
   int grp = -1, tile = 0, q0 = 0, nq = 0;   // group, tile within it, its first token and token count
   {
     int before = 0;
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
         first = __ldg(p.cu_q + s0);
         cnt = __ldg(p.cu_q + s1) - first;
       }
-      int tiles = cnt > 0 ? (cnt + p.tokens_per_tile - 1) / p.tokens_per_tile : 0;
+      int tiles = cnt > 0 ? (cnt + tokens - 1) / tokens : 0;
       int incl = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -145,14 +152,16 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   if (grp < 0) return;
   const int s0 = min(max(__ldg(p.cu_groups + grp), 0), p.num_seqs);
   const int s1 = min(max(__ldg(p.cu_groups + grp + 1), s0), p.num_seqs);
-  const int tok0 = q0 + tile * p.tokens_per_tile;
-  const int rows = min(p.tokens_per_tile, q0 + nq - tok0) * p.group;
+  // row tile X starts at token tok0 + X tokens_per_tile and has rows_of(X) rows
+  const int tok0 = q0 + tile * tokens, n_tok = q0 + nq - tok0;
+  auto rows_of = [&](int X) { return max(0, min(p.tokens_per_tile, n_tok - X * p.tokens_per_tile)) * p.group; };
+  const bool two = NT == 2 && n_tok > p.tokens_per_tile;
   const int plen = prefix_keys(p.prefix_lens, grp, p.page_size, p.max_pages);
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
-  uint64_t *q_full = bars, *q_conv = bars + 1, *k_full = bars + 2, *k_empty = k_full + NS, *k_stage = k_empty + NS,
+  uint64_t *q_full = bars, *q_conv = bars + 1, *k_full = q_conv + NT, *k_empty = k_full + NS, *k_stage = k_empty + NS,
            *v_full = k_stage + NS, *v_empty = v_full + NS, *v_stage = v_empty + NS, *s_full = v_stage + NS,
-           *p_full = s_full + 1, *o_done = p_full + 1, *sc_full = o_done + 1;
+           *p_full = s_full + NT, *o_done = p_full + NT, *sc_full = o_done + NT;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::kOffMisc + 8);
   int *range = reinterpret_cast<int *>(smem + Cfg::kOffMisc + 16);   // keys that any row sees
@@ -162,7 +171,6 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     *abort_flag = 0;
     const uint32_t n_fill = p.gather ? 32u : 1u;
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_conv), 128);
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(k_full + i), KV ? 4 * KC : n_fill);
       mbar_init(smem_u32(k_empty + i), 1);
@@ -171,22 +179,26 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
       mbar_init(smem_u32(v_empty + i), 1);
       mbar_init(smem_u32(v_stage + i), n_fill);
     }
-    mbar_init(smem_u32(s_full), 1);
-    mbar_init(smem_u32(p_full), 128);
-    mbar_init(smem_u32(o_done), 1);
+    for (int X = 0; X < NT; ++X) {
+      mbar_init(smem_u32(q_conv + X), 128);
+      mbar_init(smem_u32(s_full + X), 1);
+      mbar_init(smem_u32(p_full + X), 128);
+      mbar_init(smem_u32(o_done + X), 1);
+    }
     for (int i = 0; i < Cfg::NSS; ++i) mbar_init(smem_u32(sc_full + i), 2);
     fence_mbar_init();
   }
   __syncthreads();
-  // Row r < rows: token tok0 + r / group, head hk * group + r % group, and the
-  // keys [row_lo, row_hi) of the prefix it sees.  Rows past the last see
-  // everything (they are never stored and must force no masking).
+  // Softmax thread r of tile X: token tok0 + X tokens_per_tile + r / group, head
+  // hk * group + r % group, and the keys [row_lo, row_hi) of the prefix it sees.
+  // Rows past the last see everything (they are never stored and must force no
+  // masking).
   int row_lo = 0, row_hi = INT_MAX, ip = 0;
-  if (threadIdx.x < 128) {
-    const int r = threadIdx.x;
+  if (threadIdx.x < NT * 128) {
+    const int X = threadIdx.x >> 7, r = threadIdx.x & 127, rows = rows_of(X);
     // the row's sequence: the last that starts at or before its token, counted
     // by the warp 32 sequences at a time
-    const int tok = tok0 + min(r, rows - 1) / p.group;
+    const int tok = tok0 + X * p.tokens_per_tile + min(r, max(rows - 1, 0)) / p.group;
     int b = s0 - 1;
     for (int i0 = s0; i0 < s1; i0 += 32) {
       const int start = i0 + lane < s1 ? __ldg(p.cu_q + i0 + lane) : INT_MAX;
@@ -223,12 +235,12 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     kt_hi = min(e, kt_lo + per);
   }
   if (kt_hi <= kt_lo) {
-    for (int r = threadIdx.x; r < rows; r += Cfg::kThreads)
+    for (int r = threadIdx.x; r < min(n_tok, tokens) * p.group; r += Cfg::kThreads)
       p.lse_part[((int64_t)split * p.hq + hk * p.group + r % p.group) * p.total_q + tok0 + r / p.group] = -INFINITY;
     return;
   }
   const int n_tiles = kt_hi - kt_lo;
-  if (warp == 5) {
+  if (warp == Cfg::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -250,17 +262,19 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     return pg;
   };
 
-  if (warp >= 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
+  if (warp >= Cfg::kProducerWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
 
-  if (warp == 4) {
+  if (warp == Cfg::kProducerWarp) {
     // ------------------------------------------------ producer: Q, K, V --
     if (lane == 0) {
       prefetch_tmap(&tm_q);
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
-      mbar_expect_tx(smem_u32(q_full), (uint32_t)(KC * p.tokens_per_tile * p.group * 128));
-      for (int c = 0; c < KC; ++c)
-        tma_load_3d(smem_u32(sQ + c * Cfg::kChunkBytes), &tm_q, smem_u32(q_full), c * 64, hk * p.group, tok0);
+      mbar_expect_tx(smem_u32(q_full), (uint32_t)((two ? 2 : 1) * KC * p.tokens_per_tile * p.group * 128));
+      for (int X = 0; X < (two ? 2 : 1); ++X)
+        for (int c = 0; c < KC; ++c)
+          tma_load_3d(smem_u32(sQ + X * Cfg::kTileBytes + c * Cfg::kChunkBytes), &tm_q, smem_u32(q_full), c * 64,
+                      hk * p.group, tok0 + X * p.tokens_per_tile);
     }
     uint64_t *kb = KV ? k_stage : k_full, *vb = KV ? v_stage : v_full;
     bool ok = true;
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
         }
     }
     if (lane == 0) mbar_drain(smem_u32(q_full), 0);
-  } else if (warp == 5) {
+  } else if (warp == Cfg::kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
     if (lane == 0) {
       constexpr uint32_t id_qk = KV ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
@@ -363,53 +377,69 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
       const uint32_t hi = (uint32_t)(dq >> 32), lo_q = (uint32_t)dq;
       const uint32_t lo_k = (uint32_t)smem_desc_sw128(smem_u32(sK), 16, 1024);
       const uint32_t lo_v = (uint32_t)dv, hi_v = (uint32_t)(dv >> 32);
-      auto qk = [&](int st) {
-        uint32_t a = lo_q, b = lo_k + (uint32_t)(st * (Cfg::kTileBytes >> 4));
+      auto qk = [&](int X, int st) {
+        uint32_t a = lo_q + (uint32_t)(X * (Cfg::kTileBytes >> 4)), b = lo_k + (uint32_t)(st * (Cfg::kTileBytes >> 4));
+        const uint32_t d = tmem + X * 128u;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          if (ks == 0) mma_ss_w<0>(tmem, a, hi, b, hi, id_qk);
-          else mma_ss_w<1>(tmem, a, hi, b, hi, id_qk);
+          if (ks == 0) mma_ss_w<0>(d, a, hi, b, hi, id_qk);
+          else mma_ss_w<1>(d, a, hi, b, hi, id_qk);
           const uint32_t step = ((ks + 1) & 3) ? 2u : (uint32_t)((128 * 128 - 96) >> 4);
           a += step;
           b += step;
         }
-        tc_commit(smem_u32(s_full));
-        tc_commit(smem_u32(k_empty + st));
+        tc_commit(smem_u32(s_full + X));
+      };
+      auto pv = [&](int X, int st, int j) {
+        uint32_t b = lo_v + (uint32_t)(st * (Cfg::kTileBytes >> 4));
+        const uint32_t a = tmem + X * 128u, d = tmem + NT * 128u + X * 128u;
+#pragma unroll
+        for (int ks = 0; ks < kBlockN / 16; ++ks) {
+          mma_ts_w(d, a + ks * 8, b, hi_v, id_pv, (ks > 0 || j > 0) ? 1u : 0u);
+          b += (16 * 128) >> 4;
+        }
+        tc_commit(smem_u32(o_done + X));
       };
       bool ok = mbar_wait(smem_u32(KV ? q_conv : q_full), 0, abort_flag, p.err);
+      if (ok && KV && two) ok = mbar_wait(smem_u32(q_conv + 1), 0, abort_flag, p.err);
       if (ok) ok = mbar_wait(smem_u32(k_full), 0, abort_flag, p.err);
       if (ok) {
         tc_fence_after();
-        qk(0);
+        qk(0, 0);
+        if (two) qk(1, 0);
+        tc_commit(smem_u32(k_empty));
       }
       for (int j = 0; ok && j < n_tiles; ++j) {
         const int st = j % NS, sn = (j + 1) % NS;
+        const bool more = j + 1 < n_tiles;
         if (!(ok = mbar_wait(smem_u32(v_full + st), (j / NS) & 1, abort_flag, p.err))) break;
         if (!(ok = mbar_wait(smem_u32(p_full), j & 1, abort_flag, p.err))) break;
         tc_fence_after();
-        uint32_t b = lo_v + (uint32_t)(st * (Cfg::kTileBytes >> 4));
-#pragma unroll
-        for (int ks = 0; ks < kBlockN / 16; ++ks) {
-          mma_ts_w(tmem + 128, tmem + ks * 8, b, hi_v, id_pv, (ks > 0 || j > 0) ? 1u : 0u);
-          b += (16 * 128) >> 4;
-        }
-        tc_commit(smem_u32(o_done));
-        tc_commit(smem_u32(v_empty + st));
-        if (j + 1 < n_tiles) {
+        pv(0, st, j);
+        if (!two) tc_commit(smem_u32(v_empty + st));
+        if (more) {
           if (!(ok = mbar_wait(smem_u32(k_full + sn), ((j + 1) / NS) & 1, abort_flag, p.err))) break;
           tc_fence_after();
-          qk(sn);
+          qk(0, sn);
         }
+        if (two) {
+          if (!(ok = mbar_wait(smem_u32(p_full + 1), j & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          pv(1, st, j);
+          tc_commit(smem_u32(v_empty + st));
+          if (more) qk(1, sn);
+        }
+        if (more) tc_commit(smem_u32(k_empty + sn));
       }
     }
-  } else if (warp >= 6) {
+  } else if (warp >= Cfg::kFirstConverter) {
     // ---------------------------------------- converters (byte caches) --
     // Slices of 32 rows x 64 columns, K's then V's of a tile, in turn to the
     // six warps.  A slice's bytes lie in the upper half of its own
     // f16 output: step t writes rows 8t..8t+7, whose 1 KB overlaps only
     // staging rows that earlier steps (or this step, before its writes) read.
     if constexpr (KV != 0) {
-      const int cw = warp - 6;
+      const int cw = warp - Cfg::kFirstConverter;
       // the first two warps bring the K and the V scales of a tile, one tile ahead
       const float *sc_src = cw == 1 ? p.v_scale : p.k_scale;
       auto scales = [&](int kt, float (&s)[4]) {
@@ -469,18 +499,19 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   } else {
     // ---------------------------------------------------------- softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsSoftmax));
-    const int r = threadIdx.x;
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const uint32_t sa = tmem + lane_base, oa = tmem + lane_base + 128;
+    const int X = warp >> 2, r = threadIdx.x & 127, rows = rows_of(X);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sa = tmem + lane_base + X * 128u, oa = tmem + lane_base + NT * 128u + X * 128u;
     bool ok = true;
+    const int n_steps = rows > 0 ? n_tiles : 0;   // a second tile without rows takes no part
     float rowf = 1.f;
     if constexpr (KV != 0) {
       // Q to f16 in place, with a power-of-two factor per row (max|q| 2^e in
       // [2^14, 2^15)); row r owns 128 bytes of each block, visited from chunk
       // r mod 8 on so that a warp's accesses spread over all banks.
       ok = mbar_wait(smem_u32(q_full), 0, abort_flag, p.err);
-      if (ok) {
-        uint8_t *qrow = sQ + r * 128;
+      if (ok && rows > 0) {
+        uint8_t *qrow = sQ + X * Cfg::kTileBytes + r * 128;
         float amax = 0.f;
 #pragma unroll
         for (int c = 0; c < KC; ++c)
@@ -511,7 +542,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
           }
         fence_proxy_async_smem();
       }
-      mbar_arrive(smem_u32(q_conv));
+      mbar_arrive(smem_u32(q_conv + X));
     }
     const float sl2 = p.scale_log2 * rowf;
     const float c2u = 2.f * kLog2e * p.softcap_arg * rowf;
@@ -519,7 +550,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
     constexpr bool raw = MOD == 0 && KV == 0;
     const float cexp = raw ? sl2 : 1.f;
     float m_ref = -INFINITY, l = 0.f;
-    for (int j = 0; ok && j < n_tiles; ++j) {
+    for (int j = 0; ok && j < n_steps; ++j) {
       const int j0 = (kt_lo + j) * kBlockN;
       const float *ks = sSc + (j % Cfg::NSS) * 256, *vs = ks + 128;
       float lv = 0.f;      // log2 of the tile's largest v_scale (held above 2^-40, see below)
@@ -534,7 +565,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
         lv = __log2f(fminf(fmaxf(mv, 0x1p-40f), 0x1p40f));
       }
       const bool need_mask = __any_sync(0xffffffffu, j0 < row_lo || j0 + kBlockN > row_hi);
-      ok = mbar_wait(smem_u32(s_full), j & 1, abort_flag, p.err);
+      ok = mbar_wait(smem_u32(s_full + X), j & 1, abort_flag, p.err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -656,7 +687,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (warp_need && j > 0) {
-        ok = mbar_wait(smem_u32(o_done), (j - 1) & 1, abort_flag, p.err);
+        ok = mbar_wait(smem_u32(o_done + X), (j - 1) & 1, abort_flag, p.err);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
@@ -672,16 +703,16 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(smem_u32(p_full));
+      mbar_arrive(smem_u32(p_full + X));
     }
     // -------------------------------------------------------- epilogue --
-    if (ok) {
-      ok = mbar_wait(smem_u32(o_done), (n_tiles - 1) & 1, abort_flag, p.err);
+    if (ok && n_steps > 0) {
+      ok = mbar_wait(smem_u32(o_done + X), (n_tiles - 1) & 1, abort_flag, p.err);
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
         const bool has = l > 0.f;
         const float inv = has ? 1.f / l : 0.f;
-        const int64_t t = (int64_t)tok0 + r / p.group;
+        const int64_t t = (int64_t)tok0 + X * p.tokens_per_tile + r / p.group;
         const int h = hk * p.group + r % p.group;
         float *dst = p.o_part + (((int64_t)split * p.total_q + t) * p.hq + h) * D;
 #pragma unroll
@@ -703,7 +734,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == Cfg::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmemCols);
   }

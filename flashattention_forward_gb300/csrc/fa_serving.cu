@@ -250,7 +250,10 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   if (!launch->workspace || launch->workspace_bytes < need)
     return fail(FA_ERR_INVALID_ARG, "this call needs a workspace of %zu bytes (fa_shared_prefix_workspace_bytes)", need);
   if ((uintptr_t)launch->workspace & 255) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const int64_t tiles = (Tq + 128 / group - 1) / (128 / group) + prefix->num_groups - 1;
+  // CTAs along the rows: one (bf16) or two (byte caches) tiles each, every group
+  // with at most one that is not full
+  const int64_t cta_tokens = (128 / group) * (k_cache->dtype == FA_BF16 ? 1 : 2);
+  const int64_t tiles = (Tq + cta_tokens - 1) / cta_tokens + prefix->num_groups - 1;
   if (tiles > 65535) return fail(FA_ERR_UNSUPPORTED, "too many query tiles (rows / 128 + groups)");
 
   window = clamp_window(window);
@@ -693,11 +696,14 @@ size_t fa_shared_prefix_workspace_bytes(const fa_launch_t *launch, const fa_shar
   return part_bytes((int64_t)prefix->num_splits + launch->num_splits, launch->total_q, hq, dv, nullptr);
 }
 
-int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq, int32_t hkv) {
+int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq, int32_t hkv,
+                                        int32_t kv_dtype) {
   if (total_q <= 0 || num_groups <= 0 || hkv <= 0 || hq <= 0 || hq % hkv || max_len <= 0) return 1;
-  const int64_t tpt = std::max(1, 128 / (hq / hkv));
-  const int64_t tiles = std::max<int64_t>((total_q + tpt - 1) / tpt, num_groups) * hkv;
-  const int64_t by_sms = 2 * (int64_t)sm_count() / tiles;   // one wave at two CTAs per SM
+  // one wave of CTAs: two per SM of 128 rows each (bf16), or one of 256
+  const bool bf16 = kv_dtype == FA_BF16;
+  const int64_t tokens = std::max(1, 128 / (hq / hkv)) * (bf16 ? 1 : 2);
+  const int64_t tiles = std::max<int64_t>((total_q + tokens - 1) / tokens, num_groups) * hkv;
+  const int64_t by_sms = (bf16 ? 2 : 1) * (int64_t)sm_count() / tiles;
   const int64_t by_keys = ((int64_t)max_len + 127) / 128;
   return (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(by_sms, by_keys), 64));
 }

@@ -458,7 +458,7 @@ FA_API size_t fa_shared_prefix_workspace_bytes(const fa_launch_t *launch, const 
  * the keys behind it (max_own_len: the longest sequence's such keys; total_own:
  * their sum over the sequences, 0 if unknown).  Both are >= 1. */
 FA_API int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq,
-                                        int32_t hkv);
+                                        int32_t hkv, int32_t kv_dtype);
 FA_API int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max_own_len, int64_t total_own, int32_t hkv);
 
 /*
