@@ -26,10 +26,12 @@
 // Byte caches (KV 1 e4m3, 2 int8): two tiles A and B per CTA, each with its
 // softmax warpgroup, share every K/V tile, which halves the conversion per
 // product:  QK_A(0) QK_B(0) | PV_A(0) QK_A(1) PV_B(0) QK_B(1) | ...  Six
-// converter warps turn the staged bytes into f16 (exact) in place; k_scale multiplies the scores and v_scale the
-// weights in fp32.  The reference of the exponentials includes the tile's
-// largest v_scale, so that the scaled weights use f16's range whatever the
-// magnitude of V.
+// converter warps turn the staged bytes into f16 in place: K exactly (k_scale
+// multiplies the scores in fp32), V times v_scale 2^-E, with E one per tile of
+// 128 keys, so that f16 holds it whatever the magnitude of V; 2^E joins the
+// exponent of the tile's weights.  (Scales that belong to a column cost every
+// softmax warp 128 shared-memory cycles per tile; with both kept that way the
+// kernel spent half its time on them.)
 #pragma once
 #include <climits>
 
@@ -69,12 +71,13 @@ struct PrefixCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = NT * kTileBytes;
   static constexpr int kOffV = kOffK + NS * kTileBytes;
-  // byte caches: scales of NSS tiles, [128 of K, 128 of V] each.  Tile j's take
+  // byte caches: scales of NSS tiles, [128 of K, 128 of V (f16 pairs), E] each.  Tile j's take
   // the slot of tile j - NS - 1: its K bytes landed after the QKs of tile
   // j - NS, which were issued after the softmax of tile j - NS - 1.
   static constexpr int NSS = NS + 1;
   static constexpr int kOffSc = kOffV + NS * kTileBytes;
-  static constexpr int kOffBar = kOffSc + (KV ? NSS * 256 * 4 : 0);
+  static constexpr int kScWords = 260;
+  static constexpr int kOffBar = kOffSc + (KV ? NSS * kScWords * 4 : 0);
   static constexpr int kNumBars = 1 + NT + 6 * NS + 3 * NT + NSS;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
@@ -90,6 +93,15 @@ struct PrefixCfg {
   static_assert(kCtasPerSm * kPoolNeeded <= 65536, "register file");
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
 };
+
+// Packed fp32 products a *= b.
+__device__ __forceinline__ void prefix_mul2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y, r;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
 
 __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
@@ -251,15 +263,16 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   uint8_t *sQ = smem + Cfg::kOffQ, *sK = smem + Cfg::kOffK, *sV = smem + Cfg::kOffV;
   float *sSc = reinterpret_cast<float *>(smem + Cfg::kOffSc);
   const int32_t *bt = p.block_table + (int64_t)s0 * p.bt_stride;   // the group's first sequence
-  // page of prefix key `key`; -1 past the prefix (zero rows) or outside the pool (flagged)
-  auto page_of = [&](int key) -> int {
-    if (key >= plen) return -1;
-    const int pg = __ldg(bt + (key >> p.page_shift));
-    if (pg < 0 || pg >= p.n_pages) {
-      record_error(p.err, kErrBounds);
-      return -1;
-    }
-    return pg;
+  // Page of prefix key `key`, looked up ahead of its use: nothing here waits for
+  // the value.  checked(): -1 (rows of zeros) past the prefix, or outside the
+  // pool, which sets `bad`.
+  constexpr int kNoPage = INT_MIN;
+  auto page_of = [&](int key) { return key < plen ? __ldg(bt + (key >> p.page_shift)) : kNoPage; };
+  bool bad = false;
+  auto checked = [&](int pg) {
+    const bool ok = pg >= 0 && pg < p.n_pages;
+    bad = bad || (!ok && pg != kNoPage);
+    return ok ? pg : -1;
   };
 
   if (warp >= Cfg::kProducerWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsOther));
@@ -287,10 +300,12 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       // V up to j-NS.
       auto pages = [&](int kt, int (&pg)[4]) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) pg[u] = kt < kt_hi ? page_of(kt * kBlockN + lane + 32 * u) : -1;
+        for (int u = 0; u < 4; ++u) pg[u] = kt < kt_hi ? page_of(kt * kBlockN + lane + 32 * u) : kNoPage;
       };
       int pg[4], pgn[4];
       pages(kt_lo, pg);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) pg[u] = checked(pg[u]);
       for (; ok && j < n_tiles; ++j) {
         const int st = j % NS, key0 = (kt_lo + j) * kBlockN;
         pages(kt_lo + j + 1, pgn);
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         }
         gp.commit(smem_u32(vb + st));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) pg[u] = pgn[u];
+        for (int u = 0; u < 4; ++u) pg[u] = checked(pgn[u]);
       }
       gp.drain();
     } else {
@@ -323,7 +338,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       // page ids are read one tile ahead.
       const int rb = p.rows_per_box, r0 = lane * rb;
       const bool boxer = r0 < kBlockN;
-      auto page_at = [&](int kt) { return (boxer && kt < kt_hi) ? page_of(kt * kBlockN + r0) : -1; };
+      auto page_at = [&](int kt) { return (boxer && kt < kt_hi) ? page_of(kt * kBlockN + r0) : kNoPage; };
       constexpr uint32_t kBytes = KV ? 128u * D : (uint32_t)Cfg::kTileBytes;
       auto load = [&](const CUtensorMap *tm, uint8_t *dst, uint64_t *bar, int kt, int pg) {
         if (!boxer) return;
@@ -336,7 +351,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
           tma_load_4d(smem_u32(at), tm, smem_u32(bar), c * 64, hk, slot, pg);
         }
       };
-      int pg = page_at(kt_lo);
+      int pg = checked(page_at(kt_lo));
       for (; ok && j < n_tiles; ++j) {
         const int st = j % NS, kt = kt_lo + j;
         const int pg_next = page_at(kt + 1);
@@ -357,7 +372,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
           break;
         }
         load(&tm_v, sV + st * Cfg::kTileBytes, vb + st, kt, pg);
-        pg = pg_next;
+        pg = checked(pg_next);
       }
       // copies in flight land before the CTA ends, whatever the others do
       if (lane == 0)
@@ -367,6 +382,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         }
     }
     if (lane == 0) mbar_drain(smem_u32(q_full), 0);
+    if (bad) record_error(p.err, kErrBounds);
   } else if (warp == Cfg::kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
     if (lane == 0) {
@@ -442,27 +458,57 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       const int cw = warp - Cfg::kFirstConverter;
       // the first two warps bring the K and the V scales of a tile, one tile ahead
       const float *sc_src = cw == 1 ? p.v_scale : p.k_scale;
-      auto scales = [&](int kt, float (&s)[4]) {
+      // (their pages two)
+      auto pages = [&](int kt, int (&pg)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pg[u] = cw < 2 && kt < kt_hi ? page_of(kt * kBlockN + lane + 32 * u) : kNoPage;
+      };
+      auto scales = [&](int kt, const int (&pg)[4], float (&s)[4]) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          s[u] = 0.f;
-          if (cw > 1 || kt >= kt_hi) continue;
-          const int key = kt * kBlockN + lane + 32 * u;
-          const int pg = page_of(key);
-          if (pg >= 0) s[u] = __ldg(sc_src + ((int64_t)pg * p.page_size + (key & (p.page_size - 1))) * p.hkv + hk);
+          const int key = kt * kBlockN + lane + 32 * u, at = checked(pg[u]);
+          s[u] = at >= 0 ? __ldg(sc_src + ((int64_t)at * p.page_size + (key & (p.page_size - 1))) * p.hkv + hk) : 0.f;
         }
       };
+      int pg[4];
       float sc[4], scn[4];
-      scales(kt_lo, sc);
+      pages(kt_lo, pg);
+      scales(kt_lo, pg, sc);
+      pages(kt_lo + 1, pg);
       bool ok = true;
       for (int j = 0; ok && j < n_tiles; ++j) {
         const int st = j % NS;
-        scales(kt_lo + j + 1, scn);
+        scales(kt_lo + j + 1, pg, scn);
+        pages(kt_lo + j + 2, pg);
+        float *slot = sSc + (j % Cfg::NSS) * Cfg::kScWords;
         for (int half = 0; ok && half < 2; ++half) {
           uint64_t *stage = half ? v_stage : k_stage, *full = half ? v_full : k_full;
           ok = mbar_wait(smem_u32(stage + st), (j / NS) & 1, abort_flag, p.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if (half == 0 && cw == 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) slot[lane + 32 * u] = sc[u];
+          } else if (half == 0 && cw == 1) {
+            // E: the largest |v_scale| is below 2^E (E held within +-40)
+            float mv = fmaxf(fmaxf(fabsf(sc[0]), fabsf(sc[1])), fmaxf(fabsf(sc[2]), fabsf(sc[3])));
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            const int e = min(max((int)((__float_as_uint(mv) >> 23) & 0xFF) - 126, -40), 40);
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) slot[128 + lane + 32 * u] = __uint_as_float(pack_f16x2(sc[u] * f, sc[u] * f));
+            if (lane == 0) slot[256] = (float)e;
+          }
+          if (half == 0 && cw < 2) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(sc_full + j % Cfg::NSS));
+          }
+          if (half == 1) {   // every converter needs the V scales
+            ok = mbar_wait(smem_u32(sc_full + j % Cfg::NSS), (j / Cfg::NSS) & 1, abort_flag, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
           uint8_t *tile_base = (half ? sV : sK) + st * Cfg::kTileBytes;
           for (int sl = (cw + (half ? 4 * KC : 0)) % Cfg::kConverters; sl < 4 * KC; sl += Cfg::kConverters) {
             uint8_t *base = tile_base + (sl >> 2) * Cfg::kChunkBytes + (sl & 3) * 4096;
@@ -476,6 +522,11 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
               dec_bytes4_to_f16<KV>(raw.y, h[2], h[3]);
               dec_bytes4_to_f16<KV>(raw.z, h[4], h[5]);
               dec_bytes4_to_f16<KV>(raw.w, h[6], h[7]);
+              if (half) {
+                const uint32_t f = __float_as_uint(slot[128 + (sl & 3) * 32 + rr]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(f));
+              }
               __syncwarp();   // every lane has read this step's rows
               *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part)) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -483,13 +534,6 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(full + st));
-          }
-          if (half == 0 && cw < 2) {
-            float *dst = sSc + (j % Cfg::NSS) * 256 + cw * 128;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) dst[lane + 32 * u] = sc[u];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(sc_full + j % Cfg::NSS));
           }
         }
 #pragma unroll
@@ -546,23 +590,18 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
     }
     const float sl2 = p.scale_log2 * rowf;
     const float c2u = 2.f * kLog2e * p.softcap_arg * rowf;
-    // plain bf16 scores stay raw, the scale rides in the exponent's FMA
-    constexpr bool raw = MOD == 0 && KV == 0;
+    // plain scores keep their scale for the exponent's FMA
+    constexpr bool raw = MOD == 0;
     const float cexp = raw ? sl2 : 1.f;
     float m_ref = -INFINITY, l = 0.f;
     for (int j = 0; ok && j < n_steps; ++j) {
       const int j0 = (kt_lo + j) * kBlockN;
-      const float *ks = sSc + (j % Cfg::NSS) * 256, *vs = ks + 128;
-      float lv = 0.f;      // log2 of the tile's largest v_scale (held above 2^-40, see below)
+      const float *ks = sSc + (j % Cfg::NSS) * Cfg::kScWords;
+      float E = 0.f;       // byte caches: V stands at 2^-E
       if constexpr (KV != 0) {
         ok = mbar_wait(smem_u32(sc_full + j % Cfg::NSS), (j / Cfg::NSS) & 1, abort_flag, p.err);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        const float4 v4 = *reinterpret_cast<const float4 *>(vs + 4 * lane);
-        float mv = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-        // exp2(s - m) of the row sum is then at most 2^40 above its usual range
-        lv = __log2f(fminf(fmaxf(mv, 0x1p-40f), 0x1p40f));
+        E = ks[256];
       }
       const bool need_mask = __any_sync(0xffffffffu, j0 < row_lo || j0 + kBlockN > row_hi);
       ok = mbar_wait(smem_u32(s_full + X), j & 1, abort_flag, p.err);
@@ -578,21 +617,18 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         tmem_ld32(sa + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(v + 32));
         tmem_wait_ld();
         const int jc = j0 + hf * 64;
+        if constexpr (KV != 0) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(ks + hf * 64 + e);
+            prefix_mul2(v[e], v[e + 1], k4.x, k4.y);
+            prefix_mul2(v[e + 2], v[e + 3], k4.z, k4.w);
+          }
+        }
         if constexpr (!raw) {
           const float f = MOD == 2 ? c2u : sl2;
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            if constexpr (KV != 0) {
-              const float4 k4 = *reinterpret_cast<const float4 *>(ks + hf * 64 + e);
-              v[e] *= k4.x * f;
-              v[e + 1] *= k4.y * f;
-              v[e + 2] *= k4.z * f;
-              v[e + 3] *= k4.w * f;
-            } else {
-              mul2(v[e], v[e + 1], f);
-              mul2(v[e + 2], v[e + 3], f);
-            }
-          }
+          for (int e = 0; e < 64; e += 2) mul2(v[e], v[e + 1], f);
           if constexpr (MOD == 2) {
             const float cl = p.softcap_log2;
 #pragma unroll
@@ -625,7 +661,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         t2[7] = t1[21];
         float hmax = fmaxf(max3(t2[0], t2[1], t2[2]), fmaxf(max3(t2[3], t2[4], t2[5]), fmaxf(t2[6], t2[7])));
         if (raw && hmax != -INFINITY) hmax *= sl2;
-        if constexpr (KV != 0) hmax += lv;
+        if constexpr (KV != 0) hmax += E;
         const float m_new = fmaxf(m_ref, hmax);
         const bool need = m_new > m_ref + kRescaleThreshold;
         if (__any_sync(0xffffffffu, need)) {
@@ -658,7 +694,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
             tmem_st32(sa, w);
           }
         }
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref - E;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
@@ -673,19 +709,15 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
             t3 = ex2(t3);
             add2(sum[0], sum[1], t0, t1_);
             add2(sum[2], sum[3], t2_, t3);
-            if constexpr (KV != 0) {
-              const float4 v4 = *reinterpret_cast<const float4 *>(vs + hf * 64 + 32 * c + e);
-              pk[e / 2] = pack_f16x2(t0 * v4.x, t1_ * v4.y);
-              pk[e / 2 + 1] = pack_f16x2(t2_ * v4.z, t3 * v4.w);
-            } else {
-              pk[e / 2] = pack_bf16x2(t0, t1_);
-              pk[e / 2 + 1] = pack_bf16x2(t2_, t3);
-            }
+            pk[e / 2] = KV ? pack_f16x2(t0, t1_) : pack_bf16x2(t0, t1_);
+            pk[e / 2 + 1] = KV ? pack_f16x2(t2_, t3) : pack_bf16x2(t2_, t3);
           }
           prefix_tmem_st16(sa + hf * 32 + c * 16, pk);
         }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // the weights carry 2^E, the row sum does not
+      l += KV ? tile_sum * __uint_as_float((uint32_t)(127 - (int)E) << 23) : tile_sum;
       if (warp_need && j > 0) {
         ok = mbar_wait(smem_u32(o_done + X), (j - 1) & 1, abort_flag, p.err);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
