@@ -128,17 +128,18 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   // ------------------------------------------------------------ work tile --
   // The CTAs' rows (NT tiles) of all groups in a row; every warp finds this one's group.
   const int tokens = NT * p.tokens_per_tile;
-  int grp = -1, tile = 0, q0 = 0, nq = 0;   // group, tile within it, its first token and token count
+  int grp = -1, tile = 0, q0 = 0, nq = 0, s0 = 0, s1 = 0, plen = 0;   // of the group: tokens, sequences, prefix
   {
     int before = 0;
     for (int g0 = 0; g0 < p.num_groups && grp < 0; g0 += 32) {
       const int g = g0 + lane;
-      int first = 0, cnt = 0;
+      int first = 0, cnt = 0, a = 0, e = 0, len = 0;
       if (g < p.num_groups) {
-        const int s0 = min(max(__ldg(p.cu_groups + g), 0), p.num_seqs);
-        const int s1 = min(max(__ldg(p.cu_groups + g + 1), s0), p.num_seqs);
-        first = __ldg(p.cu_q + s0);
-        cnt = __ldg(p.cu_q + s1) - first;
+        len = prefix_keys(p.prefix_lens, g, p.page_size, p.max_pages);
+        a = min(max(__ldg(p.cu_groups + g), 0), p.num_seqs);
+        e = min(max(__ldg(p.cu_groups + g + 1), a), p.num_seqs);
+        first = __ldg(p.cu_q + a);
+        cnt = __ldg(p.cu_q + e) - first;
       }
       int tiles = cnt > 0 ? (cnt + tokens - 1) / tokens : 0;
       int incl = tiles;
@@ -154,6 +155,9 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         tile = (int)blockIdx.z - before - __shfl_sync(0xffffffffu, incl - tiles, l);
         q0 = __shfl_sync(0xffffffffu, first, l);
         nq = __shfl_sync(0xffffffffu, cnt, l);
+        s0 = __shfl_sync(0xffffffffu, a, l);
+        s1 = __shfl_sync(0xffffffffu, e, l);
+        plen = __shfl_sync(0xffffffffu, len, l);
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -162,13 +166,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       (__ldg(p.cu_groups) != 0 || __ldg(p.cu_groups + p.num_groups) != p.num_seqs))
     record_error(p.err, kErrBounds);   // some sequence is in no group
   if (grp < 0) return;
-  const int s0 = min(max(__ldg(p.cu_groups + grp), 0), p.num_seqs);
-  const int s1 = min(max(__ldg(p.cu_groups + grp + 1), s0), p.num_seqs);
   // row tile X starts at token tok0 + X tokens_per_tile and has rows_of(X) rows
   const int tok0 = q0 + tile * tokens, n_tok = q0 + nq - tok0;
   auto rows_of = [&](int X) { return max(0, min(p.tokens_per_tile, n_tok - X * p.tokens_per_tile)) * p.group; };
   const bool two = NT == 2 && n_tok > p.tokens_per_tile;
-  const int plen = prefix_keys(p.prefix_lens, grp, p.page_size, p.max_pages);
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Cfg::kOffBar);
   uint64_t *q_full = bars, *q_conv = bars + 1, *k_full = q_conv + NT, *k_empty = k_full + NS, *k_stage = k_empty + NS,
@@ -177,6 +178,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Cfg::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Cfg::kOffMisc + 8);
   int *range = reinterpret_cast<int *>(smem + Cfg::kOffMisc + 16);   // keys that any row sees
+  const bool ranged = p.window > 0;          // rows decide which key tiles are visited
   if (threadIdx.x == 0) {
     range[0] = INT_MAX;
     range[1] = 0;
@@ -200,13 +202,17 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
     for (int i = 0; i < Cfg::NSS; ++i) mbar_init(smem_u32(sc_full + i), 2);
     fence_mbar_init();
   }
-  __syncthreads();
+  if (warp == Cfg::kMmaWarp && !ranged) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
   // Softmax thread r of tile X: token tok0 + X tokens_per_tile + r / group, head
   // hk * group + r % group, and the keys [row_lo, row_hi) of the prefix it sees.
   // Rows past the last see everything (they are never stored and must force no
-  // masking).
+  // masking).  Without a window the rows are looked up while the first keys are
+  // on their way; with one they decide the key tiles first.
   int row_lo = 0, row_hi = INT_MAX, ip = 0;
-  if (threadIdx.x < NT * 128) {
+  auto look_up_rows = [&]() {
     const int X = threadIdx.x >> 7, r = threadIdx.x & 127, rows = rows_of(X);
     // the row's sequence: the last that starts at or before its token, counted
     // by the warp 32 sequences at a time
@@ -229,19 +235,28 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       }
       if (row_hi <= row_lo) row_lo = row_hi = 0;
     }
-    int lo = (r < rows && row_hi > row_lo) ? row_lo : INT_MAX, hi = (r < rows) ? row_hi : 0;
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      atomicMin(range, lo);
-      atomicMax(range + 1, hi);
+  };
+  int seen_lo = 0, seen_hi = plen;           // keys that any row sees
+  if (ranged) {
+    __syncthreads();
+    if (threadIdx.x < NT * 128) {
+      look_up_rows();
+      const bool live = (int)(threadIdx.x & 127) < rows_of(threadIdx.x >> 7);
+      const int lo = __reduce_min_sync(0xffffffffu, live && row_hi > row_lo ? row_lo : INT_MAX);
+      const int hi = __reduce_max_sync(0xffffffffu, live ? row_hi : 0);
+      if (lane == 0) {
+        atomicMin(range, lo);
+        atomicMax(range + 1, hi);
+      }
     }
+    __syncthreads();
+    seen_lo = range[0];
+    seen_hi = range[1];
   }
-  __syncthreads();
-  // this split's key tiles, of those that some row sees
+  // this split's key tiles, of those that some row may see
   int kt_lo, kt_hi;
   {
-    const int a = range[1] > 0 ? range[0] / kBlockN : 0, e = (range[1] + kBlockN - 1) / kBlockN;
+    const int a = seen_hi > 0 ? seen_lo / kBlockN : 0, e = (seen_hi + kBlockN - 1) / kBlockN;
     const int per = e > a ? (e - a + p.num_splits - 1) / p.num_splits : 0;
     kt_lo = a + split * per;
     kt_hi = min(e, kt_lo + per);
@@ -249,10 +264,18 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   if (kt_hi <= kt_lo) {
     for (int r = threadIdx.x; r < min(n_tok, tokens) * p.group; r += Cfg::kThreads)
       p.lse_part[((int64_t)split * p.hq + hk * p.group + r % p.group) * p.total_q + tok0 + r / p.group] = -INFINITY;
+    if (!ranged) {
+      tc_fence_before();
+      __syncthreads();
+      if (warp == Cfg::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(*tmem_slot, Cfg::kTmemCols);
+      }
+    }
     return;
   }
   const int n_tiles = kt_hi - kt_lo;
-  if (warp == Cfg::kMmaWarp) {
+  if (warp == Cfg::kMmaWarp && ranged) {
     tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
     tmem_relinquish();
   }
@@ -548,6 +571,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
     const uint32_t sa = tmem + lane_base + X * 128u, oa = tmem + lane_base + NT * 128u + X * 128u;
     bool ok = true;
     const int n_steps = rows > 0 ? n_tiles : 0;   // a second tile without rows takes no part
+    if (!ranged) look_up_rows();
     float rowf = 1.f;
     if constexpr (KV != 0) {
       // Q to f16 in place, with a power-of-two factor per row (max|q| 2^e in

@@ -69,13 +69,13 @@ constexpr int kSufWarps = 4;
 template <int D, int KV>
 struct SufCfg {
   static constexpr int kRow = D * (KV ? 1 : 2);
-  static constexpr int kStages = kRow >= 128 ? 3 : 4;
+  static constexpr int kStages = kRow >= 256 ? 2 : (kRow >= 128 ? 3 : 4);
   using Ring = RowsRing<kRow, kRow, KV != 0, kStages>;
   static constexpr int NP = kRow / 64;                   // 16-byte key pieces per row and lane
   static constexpr int WV = kRow / 32;                   // 32-bit words per value row and lane
   static constexpr int kSmemBytes = kSufWarps * Ring::kBytes + 1024;
   // what the registers of one row tile allow; shared memory allows as many
-  static constexpr int kCtasPerSm = kRow >= 256 ? 2 : 4;
+  static constexpr int kCtasPerSm = kRow >= 256 ? 3 : 4;
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
 };
 
