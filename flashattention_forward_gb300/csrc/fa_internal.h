@@ -122,7 +122,7 @@ struct PrefixLaunch {
   cudaStream_t stream;
 };
 cudaError_t launch_prefix(int d, const PrefixLaunch &L);
-// Merge of num_splits partials, one warp per (row, head).
+// Merge of num_splits partials.
 cudaError_t launch_prefix_merge(int d, const float *o_part, const float *lse_part, const int32_t *cu_q, int num_seqs,
                                 int num_splits, int64_t n_rows, int hq, void *out, float *lse, cudaStream_t stream);
 

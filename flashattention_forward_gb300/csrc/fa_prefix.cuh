@@ -53,7 +53,7 @@ struct PrefixParams {
   const float *k_scale, *v_scale;
   int64_t total_q;
   int32_t hq, hkv, group, tokens_per_tile;
-  int32_t num_splits;
+  int32_t num_splits, split_tiles;   // key ranges, and the 128-key tiles of one
   float *o_part;                 // [splits of the whole call][T_q][Hq][D]; this pass writes the first num_splits
   float *lse_part;               // [splits of the whole call][Hq][T_q]
   int32_t causal, window;
@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   int kt_lo, kt_hi;
   {
     const int a = seen_hi > 0 ? seen_lo / kBlockN : 0, e = (seen_hi + kBlockN - 1) / kBlockN;
-    const int per = e > a ? (e - a + p.num_splits - 1) / p.num_splits : 0;
-    kt_lo = a + split * per;
-    kt_hi = min(e, kt_lo + per);
+    // ranges of the same length in every group, so that a long prefix gets more
+    // of them than a short one; the last takes what is left
+    kt_lo = a + split * p.split_tiles;
+    kt_hi = split == p.num_splits - 1 ? e : min(e, kt_lo + p.split_tiles);
   }
   if (kt_hi <= kt_lo) {
     for (int r = threadIdx.x; r < min(n_tok, tokens) * p.group; r += Cfg::kThreads)

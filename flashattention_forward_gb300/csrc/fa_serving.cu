@@ -255,6 +255,7 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   const int64_t cta_tokens = (128 / group) * (k_cache->dtype == FA_BF16 ? 1 : 2);
   const int64_t tiles = (Tq + cta_tokens - 1) / cta_tokens + prefix->num_groups - 1;
   if (tiles > 65535) return fail(FA_ERR_UNSUPPORTED, "too many query tiles (rows / 128 + groups)");
+  if (Tq * Hq >= (int64_t(1) << 31)) return fail(FA_ERR_UNSUPPORTED, "too many query rows");
 
   window = clamp_window(window);
   const int esz = dtype_size(k_cache->dtype), kv = kv_code(k_cache->dtype);
@@ -305,6 +306,7 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   p.group = group;
   p.tokens_per_tile = 128 / group;
   p.num_splits = Sp;
+  p.split_tiles = (int)std::max<int64_t>(1, (((int64_t)prefix->max_len + 127) / 128 + Sp - 1) / Sp);
   p.o_part = o_part;
   p.lse_part = lse_part;
   p.causal = causal != 0;
@@ -710,12 +712,13 @@ int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int
 
 int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max_own_len, int64_t total_own, int32_t hkv) {
   if (num_seqs <= 0 || hkv <= 0 || max_own_len <= 0) return 1;
-  // Ranges that make about two waves of the decode's warps (12 per SM), 64 to
-  // 1024 keys each: short ones balance ragged batches, long ones write fewer
-  // partials.
+  // Ranges for about eight warps per SM (12 or 16 fit), 64 to 512 keys each:
+  // short ones balance ragged batches, long ones write fewer partials.
+  // Measured (us, ranges per sequence 1, 2, 4, 8, 16): 64 sequences of up to 1024
+  // such keys 87, 61, 52, 54, 56; 192 of up to 2048 432, 370, 358, 350, 360.
   const double total = total_own > 0 ? (double)total_own : 0.5 * max_own_len * num_seqs;
-  double per = total * hkv / (24.0 * sm_count());
-  per = std::min(1024.0, std::max(64.0, per));
+  double per = total * hkv / (8.0 * sm_count());
+  per = std::min(512.0, std::max(64.0, per));
   return (int32_t)std::min<int64_t>(1024, std::max<int64_t>(1, (int64_t)std::ceil(max_own_len / per)));
 }
 
