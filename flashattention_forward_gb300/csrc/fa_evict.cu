@@ -28,9 +28,6 @@
 namespace fa {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelItems = 4;                        // consecutive keys per thread and step
-constexpr int kSelChunk = kSelThreads * kSelItems;
 constexpr int kBins = 2048;
 
 // The keys of sequence b, held to what the weights and the table cover.
@@ -48,45 +45,45 @@ __device__ __forceinline__ uint32_t evict_order(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix sum over the block's threads; `total` gets the sum.
+// Exclusive prefix sum over the block's T threads; `total` gets the sum.
+template <int T>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int NW = kSelThreads / 32;
-  uint32_t incl = v;
+  constexpr int NW = T / 32;
+  auto warp_scan = [&](uint32_t x) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const uint32_t incl = warp_scan(v);
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  uint32_t before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const uint32_t x = warp_sums[w];
-    if (w < warp) before += x;
-    total += x;
-  }
+  const uint32_t sums = warp_scan(lane < NW ? warp_sums[lane] : 0u);
+  total = __shfl_sync(0xffffffffu, sums, NW - 1);
+  const uint32_t before = __shfl_sync(0xffffffffu, sums, max(warp - 1, 0));
   __syncthreads();
-  return before + incl - v;
+  return (warp ? before : 0u) + incl - v;
 }
 
 // Shared memory of the selection besides the cached weights.
 struct SelShared {
   uint32_t hist[2][kBins];                          // passes alternate
-  uint32_t warp_sums[kSelThreads / 32];
+  uint32_t warp_sums[32];
   uint32_t pick[2];                                 // digit, and what is still to be taken inside it
   uint32_t count;                                   // this CTA's (sure, equal) keys
 };
 
 // The new lengths' prefix sums, by one CTA.
+template <int T>
 __device__ __forceinline__ void evict_lengths(const EvictParams &p, uint32_t *warp_sums) {
   uint32_t run = 0, total;
-  for (int base = 0; base < p.num_seqs; base += kSelThreads) {
+  for (int base = 0; base < p.num_seqs; base += T) {
     const int x = base + threadIdx.x;
     const uint32_t n = x < p.num_seqs ? (uint32_t)min(evict_keys(p, x), p.budget) : 0u;
-    const uint32_t before = block_scan(n, warp_sums, total);
+    const uint32_t before = block_scan<T>(n, warp_sums, total);
     if (x < p.num_seqs) p.cu_out[x + 1] = (int32_t)(run + before + n);
     run += total;
   }
@@ -99,8 +96,9 @@ __device__ __forceinline__ void evict_lengths(const EvictParams &p, uint32_t *wa
 // weight, so that the update in place is safe.  Rows too long for that take
 // one CTA that reads the weights again in every pass; it writes a weight only
 // behind those it has read.
-template <int CTAS, bool CACHED>
-__global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const EvictParams p) {
+template <int CTAS, bool CACHED, int T>
+__global__ void __launch_bounds__(T) fa_evict_select_kernel(const EvictParams p) {
+  constexpr int ITEMS = 8, CHUNK = T * ITEMS;       // consecutive keys per thread and step of the ordered pass
   static_assert(CACHED || CTAS == 1, "only cached segments are shared out");
   extern __shared__ float cache[];
   __shared__ SelShared sh;
@@ -108,7 +106,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
   const int tid = threadIdx.x, part = CTAS > 1 ? (int)(blockIdx.x % CTAS) : 0;
   const int hk = blockIdx.x / CTAS, b = blockIdx.y;
   if (hk == p.hkv) {
-    if (b == 0 && part == 0) evict_lengths(p, sh.warp_sums);
+    if (b == 0 && part == 0) evict_lengths<T>(p, sh.warp_sums);
     return;
   }
   const int n = evict_keys(p, b);
@@ -123,13 +121,13 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
   const int lo = cut ? max(s0, p.sink) : s1, hi = cut ? min(s1, n - p.recent) : s1;
   if (CACHED) {
 #pragma unroll 8
-    for (int j = s0 + tid; j < s1; j += kSelThreads) cache[j - s0] = w[j];
+    for (int j = s0 + tid; j < s1; j += T) cache[j - s0] = w[j];
   }
   auto weight = [&](int j) { return CACHED ? cache[j - s0] : w[j]; };
   // Threshold: competitors above it stay, and of those equal to it the first `need`.
   uint32_t need = cut ? (uint32_t)(p.budget - p.sink - p.recent) : 0u;
   uint32_t thr = 0xFFFFFFFFu;
-  for (int i = tid; i < kBins; i += kSelThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < kBins; i += T) sh.hist[0][i] = 0;
   __syncthreads();
   if (need > 0) {
     uint32_t prefix = 0, mask = 0;
@@ -139,32 +137,39 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
       const uint32_t dmask = pass == 2 ? 1023u : 2047u;
       uint32_t *hist = sh.hist[pass & 1];
 #pragma unroll 4
-      for (int j = lo + tid; j < hi; j += kSelThreads) {
+      for (int j = lo + tid; j < hi; j += T) {
         const uint32_t u = evict_order(weight(j));
         if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & dmask], 1u);
       }
       if (CTAS > 1) cg::this_cluster().sync();
       else __syncthreads();
-      // bins from the highest: thread t owns four, counted from the top
-      uint32_t c[4] = {0, 0, 0, 0}, mine, total;
-      const int top = kBins - 4 - 4 * tid;
+      // bins from the highest: thread t owns B, counted from the top
+      constexpr int B = kBins / T;
+      uint32_t c[B], mine = 0, total;
+      const int top = kBins - B - B * tid;
+#pragma unroll
+      for (int k = 0; k < B; ++k) c[k] = 0;
 #pragma unroll
       for (int x = 0; x < CTAS; ++x) {
         const uint32_t *h = CTAS > 1 ? cg::this_cluster().map_shared_rank(hist, x) : hist;
-        const uint4 v = *reinterpret_cast<const uint4 *>(h + top);
-        c[0] += v.w;
-        c[1] += v.z;
-        c[2] += v.y;
-        c[3] += v.x;
-      }
-      mine = c[0] + c[1] + c[2] + c[3];
-      // the other buffer's readers passed the barrier above
-      for (int i = tid; i < kBins; i += kSelThreads) sh.hist[(pass + 1) & 1][i] = 0;
-      uint32_t above = block_scan(mine, sh.warp_sums, total);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+        for (int q = 0; q < B / 4; ++q) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(h + top + 4 * q);
+          c[B - 1 - 4 * q] += v.x;
+          c[B - 2 - 4 * q] += v.y;
+          c[B - 3 - 4 * q] += v.z;
+          c[B - 4 - 4 * q] += v.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) mine += c[k];
+      // the other buffer's readers passed the barrier above
+      for (int i = tid; i < kBins; i += T) sh.hist[(pass + 1) & 1][i] = 0;
+      uint32_t above = block_scan<T>(mine, sh.warp_sums, total);
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
         if (above < need && need <= above + c[k]) {
-          sh.pick[0] = (uint32_t)(top + 3 - k);
+          sh.pick[0] = (uint32_t)(top + B - 1 - k);
           sh.pick[1] = need - above;
         }
         above += c[k];
@@ -187,8 +192,8 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
   if (CTAS > 1) {
     // what the segments before this one hold (a segment has at most 32767 keys)
     uint32_t mine = 0, total;
-    for (int j = s0 + tid; j < s1; j += kSelThreads) mine += classify(j, cache[j - s0]);
-    block_scan(mine, sh.warp_sums, total);
+    for (int j = s0 + tid; j < s1; j += T) mine += classify(j, cache[j - s0]);
+    block_scan<T>(mine, sh.warp_sums, total);
     if (tid == 0) sh.count = total;
     cg::this_cluster().sync();
     for (int x = 0; x < part; ++x) {
@@ -198,23 +203,23 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
     }
   }
   // One ordered pass, both counts in the halves of one word (a step has at
-  // most kSelChunk of each).
-  for (int base = s0; base < s1; base += kSelChunk) {
-    const int j0 = base + tid * kSelItems;
-    float wv[kSelItems];
-    uint32_t flag[kSelItems], mine = 0;
+  // most CHUNK of each).
+  for (int base = s0; base < s1; base += CHUNK) {
+    const int j0 = base + tid * ITEMS;
+    float wv[ITEMS];
+    uint32_t flag[ITEMS], mine = 0;
 #pragma unroll
-    for (int k = 0; k < kSelItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
       const int j = j0 + k;
       wv[k] = j < s1 ? weight(j) : 0.f;
       flag[k] = j < s1 ? classify(j, wv[k]) : 0u;
       mine += flag[k];
     }
     uint32_t total;
-    const uint32_t before = block_scan(mine, sh.warp_sums, total);   // its barriers also end this step's reads of w
+    const uint32_t before = block_scan<T>(mine, sh.warp_sums, total);   // its barriers also end this step's reads of w
     uint32_t sure = sure_run + (before & 0xFFFFu), eq = eq_run + (before >> 16);
 #pragma unroll
-    for (int k = 0; k < kSelItems; ++k) {
+    for (int k = 0; k < ITEMS; ++k) {
       if (flag[k] == 1u || (flag[k] == 0x10000u && eq < need)) {
         const uint32_t rank = sure + min(eq, need);
         if (rank < (uint32_t)n_keep) {
@@ -230,20 +235,20 @@ __global__ void __launch_bounds__(kSelThreads) fa_evict_select_kernel(const Evic
   }
   // the rest of the rows, once every weight is read
   if (!CACHED) __syncthreads();
-  for (int r = n_keep + part * kSelThreads + tid; r < p.budget; r += CTAS * kSelThreads) kept[r] = -1;
-  for (int64_t r = n_keep + part * kSelThreads + tid; r < p.extent_out; r += CTAS * kSelThreads) wo[r] = 0.f;
+  for (int r = n_keep + part * T + tid; r < p.budget; r += CTAS * T) kept[r] = -1;
+  for (int64_t r = n_keep + part * T + tid; r < p.extent_out; r += CTAS * T) wo[r] = 0.f;
   if (CTAS > 1) cg::this_cluster().sync();   // no CTA leaves while another may read its counts
 }
 
 // Cached segments: up to this many keys per CTA (two CTAs per SM), and up to
 // eight CTAs; beyond, the row streams through one CTA.
 constexpr int kSegKeys = 24 * 1024;
-// A CTA takes a row alone up to this many keys (measured: see launch_select).
-constexpr int kAloneKeys = 4096;
+// A CTA takes a row alone up to this many keys.
+constexpr int kAloneKeys = 8192;
 
-template <int CTAS, bool CACHED>
+template <int CTAS, bool CACHED, int T>
 cudaError_t select_one(const EvictLaunch &L, int64_t keys) {
-  auto kern = fa_evict_select_kernel<CTAS, CACHED>;
+  auto kern = fa_evict_select_kernel<CTAS, CACHED, T>;
   const size_t smem = CACHED ? (size_t)((keys + CTAS - 1) / CTAS + 1) * sizeof(float) : 0;
   if (smem > 30 * 1024) {   // with the static part, past the 48 KB that need no opt-in
     static unsigned long long done = 0;
@@ -252,7 +257,7 @@ cudaError_t select_one(const EvictLaunch &L, int64_t keys) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((L.p.hkv + 1) * CTAS), (unsigned)L.p.num_seqs);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(T);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = L.stream;
   cudaLaunchAttribute at[1];
@@ -265,17 +270,17 @@ cudaError_t select_one(const EvictLaunch &L, int64_t keys) {
   return cudaLaunchKernelEx(&cfg, kern, L.p);
 }
 
+// Few threads for short rows: clearing and scanning the bins is work per warp.
 cudaError_t launch_select(const EvictLaunch &L) {
   const int64_t keys = std::min(L.p.max_keys, L.p.extent_in);
-  if (keys > 8 * (int64_t)kSegKeys) return select_one<1, false>(L, keys);
-  if (keys > 4 * kAloneKeys) return select_one<8, true>(L, keys);
-  if (keys > 2 * kAloneKeys) return select_one<4, true>(L, keys);
-  if (keys > kAloneKeys) return select_one<2, true>(L, keys);
-  return select_one<1, true>(L, keys);
+  if (keys > 8 * (int64_t)kSegKeys) return select_one<1, false, 512>(L, keys);
+  if (keys > 4 * kAloneKeys) return select_one<8, true, 512>(L, keys);
+  if (keys > kAloneKeys) return select_one<4, true, 512>(L, keys);
+  return select_one<1, true, 256>(L, keys);
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kMoveItems = 8;                       // 16-byte pieces per thread and block of ranks
+constexpr int kMoveWarps = 8;
+constexpr int kMoveRanks = kMoveWarps * 16;         // ranks of a block
 
 __device__ __forceinline__ uint4 ld_row(const uint8_t *a) {
   uint4 v;
@@ -287,12 +292,12 @@ __device__ __forceinline__ uint4 ld_row(const uint8_t *a) {
 }
 
 // One tensor's rows of one (sequence, kv head): P 16-byte pieces of each, from
-// byte col0 on; a block is ROWS ranks.  Indices, then pages, then data: the
-// reads of a block are in flight together.
+// byte col0 on.  A warp moves 16 rows at a time: a lane finds one row's two
+// addresses, and the lanes side by side copy its pieces.
 template <int P, bool INPLACE>
 __device__ __forceinline__ void move_rows(const EvictParams &p, uint8_t *cache, float *scale, int64_t s_page,
                                           int64_t s_slot, int64_t s_head, int b, int hk, int col0) {
-  constexpr int ROWS = kMoveThreads * kMoveItems / P;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = evict_keys(p, b);
   const int n_keep = min(n, p.budget);
   if (INPLACE && n <= p.budget) return;             // nothing moves
@@ -302,48 +307,34 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, uint8_t *cache, 
   uint8_t *head = cache + (int64_t)hk * s_head + col0;
   const int smask = p.page_size - 1;
   bool bad = false;
-  for (int r0 = (INPLACE ? p.sink : (int)blockIdx.x * ROWS); r0 < n_keep; r0 += ROWS * (INPLACE ? 1 : gridDim.x)) {
-    int j[kMoveItems], ps[kMoveItems], pd[kMoveItems];
-    uint4 v[kMoveItems];
+  for (int r0 = (INPLACE ? p.sink : (int)blockIdx.x * kMoveRanks); r0 < n_keep;
+       r0 += kMoveRanks * (INPLACE ? 1 : gridDim.x)) {
+    const int r = r0 + warp * 16 + (lane & 15);
+    int j = r < n_keep ? kept[r] : -1;
+    if (INPLACE && j == r) j = -1;                  // already there
+    const int ps = j >= 0 ? __ldg(bs + (j >> p.page_shift)) : -1, pd = j >= 0 ? __ldg(bd + (r >> p.page_shift)) : -1;
+    const bool ok = (unsigned)ps < (unsigned)p.n_pages && (unsigned)pd < (unsigned)p.n_pages;
+    bad = bad || (j >= 0 && !ok);
+    const bool go = j >= 0 && ok;
+    const uint8_t *src = go ? head + (int64_t)ps * s_page + (int64_t)(j & smask) * s_slot : nullptr;
+    uint8_t *dst = go ? head + (int64_t)pd * s_page + (int64_t)(r & smask) * s_slot : nullptr;
+    uint4 v[P / 2];
 #pragma unroll
-    for (int i = 0; i < kMoveItems; ++i) {
-      const int rr = (threadIdx.x + i * kMoveThreads) / P, r = r0 + rr;
-      j[i] = rr < ROWS && r < n_keep ? kept[r] : -1;
-      if (INPLACE && j[i] == r) j[i] = -1;          // already there
+    for (int i = 0; i < P / 2; ++i) {
+      const int e = i * 32 + lane;
+      const uint8_t *a = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)src, e / P));
+      if (a) v[i] = ld_row(a + (e % P) * 16);
     }
-#pragma unroll
-    for (int i = 0; i < kMoveItems; ++i) {
-      const int r = r0 + (threadIdx.x + i * kMoveThreads) / P;
-      ps[i] = pd[i] = -1;
-      if (j[i] >= 0) {
-        ps[i] = __ldg(bs + (j[i] >> p.page_shift));
-        pd[i] = __ldg(bd + (r >> p.page_shift));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kMoveItems; ++i) {
-      const bool ok = (unsigned)ps[i] < (unsigned)p.n_pages && (unsigned)pd[i] < (unsigned)p.n_pages;
-      bad = bad || (j[i] >= 0 && !ok);
-      if (!ok) j[i] = -1;
-      const int piece = ((threadIdx.x + i * kMoveThreads) % P) * 16;
-      if (j[i] >= 0) v[i] = ld_row(head + (int64_t)ps[i] * s_page + (int64_t)(j[i] & smask) * s_slot + piece);
-    }
-    // the scales of the block's ranks go with a row's first piece
-    float sv[kMoveItems];
-    if (scale) {
-#pragma unroll
-      for (int i = 0; i < kMoveItems; ++i)
-        if (j[i] >= 0 && (threadIdx.x + i * kMoveThreads) % P == 0)
-          sv[i] = scale[((int64_t)ps[i] * p.page_size + (j[i] & smask)) * p.hkv + hk];
-    }
+    float sv = 0.f;
+    if (scale && go && lane < 16) sv = scale[((int64_t)ps * p.page_size + (j & smask)) * p.hkv + hk];
     if (INPLACE) __syncthreads();                   // the block is read: its slots may be written
 #pragma unroll
-    for (int i = 0; i < kMoveItems; ++i) {
-      const int e = threadIdx.x + i * kMoveThreads, r = r0 + e / P;
-      if (j[i] < 0) continue;
-      *reinterpret_cast<uint4 *>(head + (int64_t)pd[i] * s_page + (int64_t)(r & smask) * s_slot + (e % P) * 16) = v[i];
-      if (scale && e % P == 0) scale[((int64_t)pd[i] * p.page_size + (r & smask)) * p.hkv + hk] = sv[i];
+    for (int i = 0; i < P / 2; ++i) {
+      const int e = i * 32 + lane;
+      uint8_t *a = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)dst, e / P));
+      if (a) *reinterpret_cast<uint4 *>(a + (e % P) * 16) = v[i];
     }
+    if (scale && go && lane < 16) scale[((int64_t)pd * p.page_size + (r & smask)) * p.hkv + hk] = sv;
   }
   if (bad) record_error(p.err, kErrBounds);
 }
@@ -351,7 +342,7 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, uint8_t *cache, 
 // Grid y: (kv head, column slice, K or V).  PK, PV: 16-byte pieces of a K and a
 // V row slice; `slices` of them make a K row (a V row has at most as many).
 template <int PK, int PV, bool INPLACE>
-__global__ void __launch_bounds__(kMoveThreads) fa_evict_move_kernel(const EvictParams p, int slices) {
+__global__ void __launch_bounds__(kMoveWarps * 32) fa_evict_move_kernel(const EvictParams p, int slices) {
   const int is_v = blockIdx.y & 1, slice = (blockIdx.y >> 1) % slices, hk = (blockIdx.y >> 1) / slices, b = blockIdx.z;
   if (is_v) {
     if (slice * PV * 16 >= p.v_row) return;
@@ -364,10 +355,9 @@ __global__ void __launch_bounds__(kMoveThreads) fa_evict_move_kernel(const Evict
 template <int PK, int PV>
 cudaError_t move_apart(const EvictLaunch &L) {
   const EvictParams &p = L.p;
-  constexpr int ROWS = kMoveThreads * kMoveItems / (PK > PV ? PK : PV);
   const int64_t most = std::min<int64_t>(p.budget, p.max_keys);
-  const unsigned x = (unsigned)std::max<int64_t>(1, (most + ROWS - 1) / ROWS);
-  fa_evict_move_kernel<PK, PV, false><<<dim3(x, 2 * p.hkv, p.num_seqs), kMoveThreads, 0, L.stream>>>(p, 1);
+  const unsigned x = (unsigned)std::max<int64_t>(1, (most + kMoveRanks - 1) / kMoveRanks);
+  fa_evict_move_kernel<PK, PV, false><<<dim3(x, 2 * p.hkv, p.num_seqs), kMoveWarps * 32, 0, L.stream>>>(p, 1);
   return cudaGetLastError();
 }
 
@@ -376,7 +366,7 @@ cudaError_t launch_move(const EvictLaunch &L) {
   if (!p.bt_out) {
     // In place a CTA walks its ranks alone; slices of 64 bytes make more CTAs.
     const int slices = p.k_row / 64;
-    fa_evict_move_kernel<4, 4, true><<<dim3(1, 2 * p.hkv * slices, p.num_seqs), kMoveThreads, 0, L.stream>>>(p, slices);
+    fa_evict_move_kernel<4, 4, true><<<dim3(1, 2 * p.hkv * slices, p.num_seqs), kMoveWarps * 32, 0, L.stream>>>(p, slices);
     return cudaGetLastError();
   }
   switch (p.k_row) {
