@@ -701,13 +701,18 @@ size_t fa_shared_prefix_workspace_bytes(const fa_launch_t *launch, const fa_shar
 int32_t fa_shared_prefix_default_splits(int64_t total_q, int32_t num_groups, int32_t max_len, int32_t hq, int32_t hkv,
                                         int32_t kv_dtype) {
   if (total_q <= 0 || num_groups <= 0 || hkv <= 0 || hq <= 0 || hq % hkv || max_len <= 0) return 1;
-  // one wave of CTAs: two per SM of 128 rows each (bf16), or one of 256
+  // One CTA per SM, of 128 rows (bf16) or 256: at most one wave, since a second
+  // doubles the time.  Two bf16 CTAs fit an SM, which pays once each has five
+  // key tiles.  Measured (us, ranges per prefix): 64 rows of 32 heads behind
+  // 8192 keys 54 (6), 50 (9), 48 (12), 49 (19); 34 rows of 12 heads behind 11
+  // key tiles 22 (2), 15.6 (6), 18.8 (12).
   const bool bf16 = kv_dtype == FA_BF16;
   const int64_t tokens = std::max(1, 128 / (hq / hkv)) * (bf16 ? 1 : 2);
   const int64_t tiles = std::max<int64_t>((total_q + tokens - 1) / tokens, num_groups) * hkv;
-  const int64_t by_sms = (bf16 ? 2 : 1) * (int64_t)sm_count() / tiles;
   const int64_t by_keys = ((int64_t)max_len + 127) / 128;
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(by_sms, by_keys), 64));
+  int64_t n = sm_count() / tiles;
+  if (bf16) n = std::max(n, std::min<int64_t>(2 * (int64_t)sm_count() / tiles, by_keys / 5));
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>(std::min(n, by_keys), 64));
 }
 
 int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max_own_len, int64_t total_own, int32_t hkv) {
