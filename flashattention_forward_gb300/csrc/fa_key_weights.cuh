@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(KwTileCfg<D>::kThreads, 2)
     }
   } else if (warp == Cfg::kMmaWarp) {
     // ----------------------------------------------------------- MMAs --
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
       const uint64_t dk = smem_desc_sw128(smem_u32(sK), 16, 1024);
       const uint32_t hi = (uint32_t)(dk >> 32), lo_k = (uint32_t)dk;

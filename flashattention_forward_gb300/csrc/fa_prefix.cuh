@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
     if (bad) record_error(p.err, kErrBounds);
   } else if (warp == Cfg::kMmaWarp) {
     // ------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t id_qk = KV ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
       constexpr uint32_t id_pv = KV ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
       const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);

@@ -93,6 +93,18 @@ def test_tile_edges(form):
         check(*case([2] if form == "rows" else [nk - 3], [nk], hq=2, hkv=1, d=64, seed=nk))
 
 
+@pytest.mark.parametrize("mod,group,page", [("none", 1, 16), ("none", 3, 0), ("alibi", 1, 64), ("softcap", 2, 1)])
+def test_tile_form_with_more_key_tiles_than_multiprocessors(mod, group, page):
+    """Ragged lengths, so that the blocks that run take over very different key tiles of the rest: many with
+    fewer query tiles than there are accumulators, some with none."""
+    g = torch.Generator().manual_seed(group)
+    q_lens = torch.randint(0, 260, (48,), generator=g).tolist()
+    k_lens = [n + int(torch.randint(0, 400, (1,), generator=g)) * (i % 3 == 0) for i, n in enumerate(q_lens)]
+    k_lens[5], k_lens[6] = 0, 3
+    q_lens[5], q_lens[7], q_lens[8] = 4, 0, 600
+    check(*case(q_lens, k_lens, hq=8 * group, hkv=8, d=64, page=page, mod=mod, seed=group))
+
+
 @pytest.mark.parametrize("form", ["rows", "tile"])
 def test_beta_out_and_strides(form):
     """Accumulation, decay, in place and apart, strided weight rows, entries past the keys."""
