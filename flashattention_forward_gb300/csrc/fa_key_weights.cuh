@@ -69,7 +69,8 @@ struct KeyWeightsParams {
 };
 
 // The lengths of one sequence, with the key count held to what the weights
-// and the page table cover (a longer sequence is flagged).
+// and the page table cover (a longer sequence is flagged; one whose query rows
+// lie outside q is flagged and adds nothing).
 struct KwSeq {
   int qa, sq, ka, sk, shift;          // shift = Sk - Sq: i' = i + shift
 };
@@ -84,6 +85,10 @@ __device__ __forceinline__ KwSeq kw_sequence(const KeyWeightsParams &p, int b) {
   if (p.block_table) cap = min(cap, p.max_pages * p.page_size);
   if (sk > cap && threadIdx.x == 0) record_error(p.err, kErrBounds);
   s.sk = (int)min((int64_t)sk, cap);
+  if (s.sq > 0 && (s.qa < 0 || (int64_t)s.qa + s.sq > p.total_q)) {
+    if (threadIdx.x == 0) record_error(p.err, kErrBounds);
+    s.sq = 0;
+  }
   return s;
 }
 

@@ -147,6 +147,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         e = min(max(__ldg(p.cu_groups + g + 1), a), p.num_seqs);
         first = __ldg(p.cu_q + a);
         cnt = __ldg(p.cu_q + e) - first;
+        if (cnt > 0 && (first < 0 || (int64_t)first + cnt > p.total_q)) {   // rows outside q
+          record_error(p.err, kErrBounds);
+          cnt = 0;
+        }
       }
       int tiles = cnt > 0 ? (cnt + tokens - 1) / tokens : 0;
       int incl = tiles;

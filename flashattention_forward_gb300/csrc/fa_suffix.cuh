@@ -113,6 +113,10 @@ __device__ __forceinline__ void suffix_warp(const CUtensorMap *tm_k, const CUten
   const int shift = sk - sq;
   int rows = sq * p.group;
   if (rows <= 0) return;
+  if (qa < 0 || (int64_t)qa + sq > p.total_q) {   // rows outside q
+    if (lane == 0) record_error(p.err, kErrBounds);
+    return;
+  }
   // lengths that the host's bounds or the page table do not cover
   if (rows > NT * 8 || sk > p.max_pages * p.page_size) {
     if (lane == 0) record_error(p.err, kErrBounds);

@@ -229,3 +229,15 @@ def test_scales_from_zero_to_large(form, kv):
     check((q.to(DEV), t["k"], lse.to(DEV), sl.cu(q_lens).to(DEV), t["cu_k"]),
           dict(max_seqlen_q=q_lens[0], max_seqlen_k=260, block_table=t["bt"], page_size=16, k_scale=t["k_scale"],
                causal=True), ref)
+
+
+@pytest.mark.parametrize("form", ["rows", "tile"])
+def test_query_rows_outside_q_are_flagged_and_add_nothing(form):
+    import flashattention_forward_gb300 as fa
+    args, kw, ref = case([1, 2] if form == "rows" else [100, 40], [100, 40])
+    args[3][2] = 1 << 20
+    kw["max_seqlen_q"] = 2 if form == "rows" else 100
+    out = fa.key_weights(*args, **kw)
+    assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
+    sl.within(out[0], ref[0][0], ref[1][0])
+    assert bool((out[1] == 0).all())

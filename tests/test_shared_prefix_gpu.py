@@ -236,3 +236,17 @@ def test_groups_that_leave_sequences_out_are_flagged():
     kw["cu_groups"][1] = 2
     fa.fwd_shared_prefix(*args, **kw)
     assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_query_rows_outside_q_are_flagged_and_not_written(kv):
+    """cu_seqlens_q that runs past T_q: the sequences before keep their results."""
+    import flashattention_forward_gb300 as fa
+    args, kw, ref = case(groups=(0, 2, 4), prefix=(300, 64), suffix=(9, 30, 6, 64), kv=kv)
+    args[3][4] = 9
+    out = torch.full((6, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((4, 6), 7.0, device=DEV)
+    fa.fwd_shared_prefix(*args, **kw, out=out[:4], lse=lse.view(-1)[:16].view(4, 4))
+    assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
+    sl.within(out[:2], ref[0][:2], ref[2][:2])
+    assert bool((out[4:] == 7).all()) and bool((lse.view(-1)[16:] == 7).all())
