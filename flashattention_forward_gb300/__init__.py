@@ -500,6 +500,12 @@ def bwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
 
 # ------------------------------------------------- around the paged decode --
 
+def _raw_stream(index: int) -> int:
+    """Handle of a device's current stream; the public call builds a Stream
+    object around it, which takes longer than a small kernel's launch."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _run_on(device: torch.device, stream, body):
     """body(stream handle) with ``device`` and ``stream`` (None: the device's
     current stream) current, so that what it allocates belongs to the stream
@@ -507,7 +513,7 @@ def _run_on(device: torch.device, stream, body):
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, not {device}")
     if stream is None and torch.cuda.current_device() == device.index:
-        return body(torch.cuda.current_stream(device.index).cuda_stream)
+        return body(_raw_stream(device.index))
     with torch.cuda.device(device):
         if stream is None:
             return body(torch.cuda.current_stream().cuda_stream)
@@ -523,7 +529,7 @@ _PAD = [(0,) * (5 - n) for n in range(6)]
 def _packer(device: torch.device):
     """pack(tensor, fa dtype or None) -> its fa_tensor_t as bytes (None for
     None); every tensor has to be on ``device``."""
-    index = device.index
+    index, put, pads, types = device.index, _TENSOR.pack, _PAD, _DT
 
     def pack(t, fa_dtype=None):
         if t is None:
@@ -531,9 +537,9 @@ def _packer(device: torch.device):
         if t.get_device() != index:
             raise ValueError(f"all tensors must be on {device}, one is on {t.device}")
         shape = t.shape
-        pad = _PAD[len(shape)]
-        return _TENSOR.pack(t.data_ptr(), _DT[t.dtype] if fa_dtype is None else fa_dtype, len(shape), *shape, *pad,
-                            *t.stride(), *pad)
+        n = len(shape)
+        pad = pads[n]
+        return put(t.data_ptr(), types[t.dtype] if fa_dtype is None else fa_dtype, n, *shape, *pad, *t.stride(), *pad)
     return pack
 
 
@@ -543,6 +549,7 @@ class _Prepared:
     def __init__(self, device, keep, result, handle):
         L = lib()
         self._device = device
+        self._index = device.index
         self._keep = keep
         self._result = result
         self._plan = handle
@@ -550,13 +557,12 @@ class _Prepared:
         self._destroy_fn = L.fa_fwd_plan_destroy
 
     def run(self, stream=None):
-        if stream is None:
-            stream = torch.cuda.current_stream(self._device)
-        if torch.cuda.current_device() == self._device.index:
-            st = self._launch_fn(self._plan, ctypes.c_void_p(stream.cuda_stream))
+        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() == self._index:
+            st = self._launch_fn(self._plan, s)
         else:
             with torch.cuda.device(self._device):
-                st = self._launch_fn(self._plan, ctypes.c_void_p(stream.cuda_stream))
+                st = self._launch_fn(self._plan, s)
         if st != FA_OK:
             _check(st)
         return self._result
@@ -744,10 +750,10 @@ def cache_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     def call(s):
         kept_ = kept
         if kept_ is None:
-            kept_ = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
+            kept_ = cu_seqlens_k.new_empty((B, Hkv, max(0, budget)))
         cu_out = cu_seqlens_k_out
         if cu_out is None:
-            cu_out = torch.empty((B + 1,), dtype=torch.int32, device=weights.device)
+            cu_out = cu_seqlens_k.new_empty((B + 1,))
         kv_dt = _kv_dtype(k_cache)
         launch = Launch(num_seqs=B, max_seqlen_q=0, max_seqlen_k=max_seqlen_k)
         pack = _packer(weights.device)
