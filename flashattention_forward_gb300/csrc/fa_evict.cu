@@ -105,7 +105,6 @@ __global__ void __launch_bounds__(T) fa_evict_select_kernel(const EvictParams p)
   namespace cg = cooperative_groups;
   const int tid = threadIdx.x, part = CTAS > 1 ? (int)(blockIdx.x % CTAS) : 0;
   const int hk = blockIdx.x / CTAS, b = blockIdx.y;
-  pdl_launch();   // the move finds its CTAs' addresses once this kernel has ended
   if (hk == p.hkv) {
     if (b == 0 && part == 0) evict_lengths<T>(p, sh.warp_sums);
     return;
@@ -344,7 +343,6 @@ __device__ __forceinline__ void move_rows(const EvictParams &p, uint8_t *cache, 
 // V row slice; `slices` of them make a K row (a V row has at most as many).
 template <int PK, int PV, bool INPLACE>
 __global__ void __launch_bounds__(kMoveWarps * 32) fa_evict_move_kernel(const EvictParams p, int slices) {
-  pdl_wait();
   const int is_v = blockIdx.y & 1, slice = (blockIdx.y >> 1) % slices, hk = (blockIdx.y >> 1) / slices, b = blockIdx.z;
   if (is_v) {
     if (slice * PV * 16 >= p.v_row) return;
@@ -359,7 +357,8 @@ cudaError_t move_apart(const EvictLaunch &L) {
   const EvictParams &p = L.p;
   const int64_t most = std::min<int64_t>(p.budget, p.max_keys);
   const unsigned x = (unsigned)std::max<int64_t>(1, (most + kMoveRanks - 1) / kMoveRanks);
-  return launch_behind(fa_evict_move_kernel<PK, PV, false>, dim3(x, 2 * p.hkv, p.num_seqs), kMoveWarps * 32, 0, L.stream, p, 1);
+  fa_evict_move_kernel<PK, PV, false><<<dim3(x, 2 * p.hkv, p.num_seqs), kMoveWarps * 32, 0, L.stream>>>(p, 1);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_move(const EvictLaunch &L) {
@@ -367,8 +366,8 @@ cudaError_t launch_move(const EvictLaunch &L) {
   if (!p.bt_out) {
     // In place a CTA walks its ranks alone; slices of 64 bytes make more CTAs.
     const int slices = p.k_row / 64;
-    return launch_behind(fa_evict_move_kernel<4, 4, true>, dim3(1, 2 * p.hkv * slices, p.num_seqs), kMoveWarps * 32, 0,
-                         L.stream, p, slices);
+    fa_evict_move_kernel<4, 4, true><<<dim3(1, 2 * p.hkv * slices, p.num_seqs), kMoveWarps * 32, 0, L.stream>>>(p, slices);
+    return cudaGetLastError();
   }
   switch (p.k_row) {
     case 64: return move_apart<4, 4>(L);

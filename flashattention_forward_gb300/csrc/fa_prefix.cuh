@@ -94,22 +94,6 @@ struct PrefixCfg {
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
 };
 
-// Packed fp32 products a *= b.
-__device__ __forceinline__ void prefix_mul2(float &a0, float &a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 x, y, r;\n\t"
-      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-      "mul.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
-}
-
-// a + b held within [0, 1].
-__device__ __forceinline__ float add_sat(float a, float b) {
-  float y;
-  asm("add.sat.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -657,8 +641,8 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float4 k4 = *reinterpret_cast<const float4 *>(ks + hf * 64 + e);
-            prefix_mul2(v[e], v[e + 1], k4.x, k4.y);
-            prefix_mul2(v[e + 2], v[e + 3], k4.z, k4.w);
+            mul2p(v[e], v[e + 1], k4.x, k4.y);
+            mul2p(v[e + 2], v[e + 3], k4.z, k4.w);
           }
         }
         if constexpr (!raw) {
@@ -701,14 +685,8 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
             for (int e = 0; e < 64; ++e) v[e] = add_sat(ex2(v[e]), 0x1p-30f);
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
-              float ab = v[e], cd = v[e + 2];
-              prefix_mul2(ab, cd, v[e + 1], v[e + 3]);
-              const float r = rcp_approx(ab * cd);
-              float rab = cd, rcd = ab;
-              mul2(rab, rcd, r);
-              float x0 = v[e + 1], x1 = v[e], x2 = v[e + 3], x3 = v[e + 2];
-              mul2(x0, x1, rab);
-              mul2(x2, x3, rcd);
+              float x0, x1, x2, x3;
+              rcp4(v[e], v[e + 1], v[e + 2], v[e + 3], x0, x1, x2, x3);
               fma2(v[e], v[e + 1], x0, x1, -0x1p-29f * cl, cl);
               fma2(v[e + 2], v[e + 3], x2, x3, -0x1p-29f * cl, cl);
             }

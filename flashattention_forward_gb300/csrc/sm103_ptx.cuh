@@ -326,6 +326,31 @@ __device__ __forceinline__ void mul2(float &a0, float &a1, float b) {
       : "+f"(a0), "+f"(a1)
       : "f"(b));
 }
+// Packed fp32 products a *= b.
+__device__ __forceinline__ void mul2p(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y, r;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+// a + b held within [0, 1].
+__device__ __forceinline__ float add_sat(float a, float b) {
+  float y;
+  asm("add.sat.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// x = 1 / a of four values by one reciprocal of their product.
+__device__ __forceinline__ void rcp4(float a0, float a1, float a2, float a3, float &x0, float &x1, float &x2, float &x3) {
+  float ab = a0, cd = a2;
+  mul2p(ab, cd, a1, a3);
+  const float r = rcp_approx(ab * cd);
+  float rab = cd, rcd = ab;
+  mul2(rab, rcd, r);
+  x0 = a1, x1 = a0, x2 = a3, x3 = a2;
+  mul2(x0, x1, rab);
+  mul2(x2, x3, rcd);
+}
 __device__ __forceinline__ void fma2v(float &a0, float &a1, float b, float c0, float c1) {
   asm("{\n\t.reg .b64 x, y, z, r;\n\t"
       "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %4};\n\t"
