@@ -748,12 +748,8 @@ def cache_evict(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     B, Hkv = weights.shape[0], weights.shape[1]
 
     def call(s):
-        kept_ = kept
-        if kept_ is None:
-            kept_ = cu_seqlens_k.new_empty((B, Hkv, max(0, budget)))
-        cu_out = cu_seqlens_k_out
-        if cu_out is None:
-            cu_out = cu_seqlens_k.new_empty((B + 1,))
+        kept_ = cu_seqlens_k.new_empty((B, Hkv, max(0, budget))) if kept is None else kept
+        cu_out = torch.empty_like(cu_seqlens_k) if cu_seqlens_k_out is None else cu_seqlens_k_out
         kv_dt = _kv_dtype(k_cache)
         launch = Launch(num_seqs=B, max_seqlen_q=0, max_seqlen_k=max_seqlen_k)
         pack = _packer(weights.device)
