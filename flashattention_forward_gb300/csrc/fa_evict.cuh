@@ -4,6 +4,9 @@
 
 namespace fa {
 
+// Weights that a CTA of a cluster holds in shared memory (two CTAs per SM).
+constexpr int kEvictSegKeys = 24 * 1024;
+
 struct EvictParams {
   const float *w;                     // [B, Hkv, extent_in]
   int64_t w_stride_b, w_stride_h, extent_in;

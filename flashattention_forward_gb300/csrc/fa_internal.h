@@ -148,6 +148,7 @@ cudaError_t launch_key_weights(int d, const KeyWeightsLaunch &L);
 
 struct EvictLaunch {
   EvictParams p;
+  int ctas;   // that share a (sequence, kv head)'s selection: 1, 4 or 8
   cudaStream_t stream;
 };
 cudaError_t launch_evict(const EvictLaunch &L);

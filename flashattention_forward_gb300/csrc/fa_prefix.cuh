@@ -18,6 +18,8 @@
 //
 // bf16 caches: one tile per CTA and two CTAs per SM, so that one CTA's softmax
 // runs under the other's products; 64 KB of K and V are in flight per CTA.
+// 6144 rows over 65536 keys, D 128: 169 us, 1220 TFLOP/s; the same with the
+// products issued behind (lane == 0) instead of an elected lane, 188 us.
 //
 // Every row has its own interval of visible keys (its sequence's length,
 // causal limit and window), so the result does not depend on the prefix lying

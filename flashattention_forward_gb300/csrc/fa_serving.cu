@@ -623,6 +623,14 @@ fa_status_t evict_build(const fa_tensor_t *weights, fa_tensor_t *weights_out, co
   p.max_keys = launch->max_seqlen_k;
   p.kept = (int32_t *)kept->data;
   p.err = error_word();
+  // A row of long weights is shared by the CTAs of a cluster where the rows do
+  // not fill the GPU by themselves (two CTAs per SM), as far as a segment fits
+  // its shared memory.  Measured (us; 1, 4, 8 CTAs): 12 rows of 30000 weights 30,
+  // 19, 21, of 100000 95, -, 28; 384 rows of 30000 67, 99, 264; 32 rows of 8192
+  // 12, 14, - .
+  const int64_t keys = std::min(p.max_keys, p.extent_in), rows = B * Hkv;
+  const auto fits = [&](int64_t ctas) { return rows * ctas <= 2 * sm_count() && keys <= ctas * fa::kEvictSegKeys; };
+  P.ev.ctas = keys > 32768 && fits(8) ? 8 : keys > 8192 && fits(4) ? 4 : 1;
   P.kind = 5;
   return FA_OK;
 }

@@ -6,7 +6,8 @@
 // (key range, kv head, sequence): keys and values come through a ring of its
 // own into MMA fragments (fa_rows.cuh), the softmax state is the warp's, and its
 // partial (O, LSE) goes to the merge that joins it with the prefix's.  No
-// barriers, and any page size.
+// barriers, and any page size.  Bound by HBM: 64 sequences of up to 1024 own
+// keys, bf16, 27 us (4.7 TB/s); 192 of up to 2048, int8, 87 us (4.6 TB/s).
 //
 //   S^T = K Q^T          M = 16 keys, N = 8 rows: lane (g, t) gets keys g, g + 8
 //                        (in the order of RowsBlocks::row) of rows 2t, 2t + 1

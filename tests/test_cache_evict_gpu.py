@@ -205,3 +205,10 @@ def test_bad_pages_and_lengths_are_flagged():
                                   max_seqlen_k=200, **kw)
         assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
         assert cu.tolist() == [0, 64, 128] and int(kept.max()) == 199
+
+
+@pytest.mark.parametrize("w_apart", [False, True])
+@pytest.mark.parametrize("lens,budget", [([9000, 8500] * 12, 3000), ([230000, 12], 120000)])
+def test_long_rows_of_one_block_each(lens, budget, w_apart):
+    """More rows than clusters are made for, and a row longer than eight blocks hold."""
+    run(lens, budget, sink=5, recent=40, hkv=4, dk=64, dv=64, page=256, seed=len(lens), w_apart=w_apart)
