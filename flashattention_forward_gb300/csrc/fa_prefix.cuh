@@ -472,9 +472,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
   } else if (warp >= Cfg::kFirstConverter) {
     // ---------------------------------------- converters (byte caches) --
     // Slices of 32 rows x 64 columns, K's then V's of a tile, in turn to the
-    // six warps.  A slice's bytes lie in the upper half of its own
-    // f16 output: step t writes rows 8t..8t+7, whose 1 KB overlaps only
-    // staging rows that earlier steps (or this step, before its writes) read.
+    // six warps.  A slice's bytes lie in the upper half of its own f16 output.
     if constexpr (KV != 0) {
       const int cw = warp - Cfg::kFirstConverter;
       // the first two warps bring the K and the V scales of a tile, one tile ahead
@@ -534,21 +532,29 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
           for (int sl = (cw + (half ? 4 * KC : 0)) % Cfg::kConverters; sl < 4 * KC; sl += Cfg::kConverters) {
             uint8_t *base = tile_base + (sl >> 2) * Cfg::kChunkBytes + (sl & 3) * 4096;
             const uint8_t *stg = base + 2048;
+            // all rows are read before any is written, so that their latencies overlap
+            const int part = lane & 3;
+            uint4 raw[4];
+            uint32_t f[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const int rr = 8 * t + (lane >> 2), part = lane & 3;
-              const uint4 raw = *reinterpret_cast<const uint4 *>(stg + rr * 64 + part * 16);
-              uint32_t h[8];
-              dec_bytes4_to_f16<KV>(raw.x, h[0], h[1]);
-              dec_bytes4_to_f16<KV>(raw.y, h[2], h[3]);
-              dec_bytes4_to_f16<KV>(raw.z, h[4], h[5]);
-              dec_bytes4_to_f16<KV>(raw.w, h[6], h[7]);
-              if (half) {
-                const uint32_t f = __float_as_uint(slot[128 + (sl & 3) * 32 + rr]);
+              const int rr = 8 * t + (lane >> 2);
+              raw[t] = *reinterpret_cast<const uint4 *>(stg + rr * 64 + part * 16);
+              f[t] = half ? __float_as_uint(slot[128 + (sl & 3) * 32 + rr]) : 0u;
+            }
+            __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(f));
+            for (int t = 0; t < 4; ++t) {
+              const int rr = 8 * t + (lane >> 2);
+              uint32_t h[8];
+              dec_bytes4_to_f16<KV>(raw[t].x, h[0], h[1]);
+              dec_bytes4_to_f16<KV>(raw[t].y, h[2], h[3]);
+              dec_bytes4_to_f16<KV>(raw[t].z, h[4], h[5]);
+              dec_bytes4_to_f16<KV>(raw[t].w, h[6], h[7]);
+              if (half) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[k]) : "r"(f[t]));
               }
-              __syncwarp();   // every lane has read this step's rows
               *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part)) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4 *>(base + sw128(rr, 2 * part + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
