@@ -33,7 +33,9 @@
 // 128 keys, so that f16 holds it whatever the magnitude of V; 2^E joins the
 // exponent of the tile's weights.  (Scales that belong to a column cost every
 // softmax warp 128 shared-memory cycles per tile; with both kept that way the
-// kernel spent half its time on them.)
+// kernel spent half its time on them.)  Bound by shared memory: per pair of
+// tiles 1536 cycles of operands, 768 of conversion, 1024 of K scales and 256 of
+// loads.  768 rows of 8 kv heads over 65536 int8 keys take 229 us, 900 TFLOP/s.
 #pragma once
 #include <climits>
 
@@ -89,12 +91,18 @@ struct PrefixCfg {
   static constexpr int kCtasPerSm = KV ? 1 : 2;
   static constexpr int kThreads = (KV ? 16 : 8) * 32, kConverters = 6;
   static constexpr int kProducerWarp = 4 * NT, kMmaWarp = 4 * NT + 1, kFirstConverter = 4 * NT + 2;
-  static constexpr int kRegsSoftmax = KV ? 152 : 200, kRegsOther = KV ? 104 : 56;
+  static constexpr int kRegsSoftmax = KV ? 168 : 200, kRegsOther = KV ? 88 : 56;
   static constexpr int kPoolNeeded = NT * 128 * kRegsSoftmax + (kThreads - NT * 128) * kRegsOther;
   static constexpr uint32_t kTmemCols = NT * 256;      // S (and P) of each tile, then O of each
   static_assert(kCtasPerSm * kPoolNeeded <= 65536, "register file");
   static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 233472, "shared memory");
 };
+
+__device__ __forceinline__ float4 prefix_lds16(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
 
 __device__ __forceinline__ void prefix_tmem_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
@@ -625,6 +633,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
     for (int j = 0; ok && j < n_steps; ++j) {
       const int j0 = (kt_lo + j) * kBlockN;
       const float *ks = sSc + (j % Cfg::NSS) * Cfg::kScWords;
+      const uint32_t ks_at = smem_u32(ks);
       float E = 0.f;       // byte caches: V stands at 2^-E
       if constexpr (KV != 0) {
         ok = mbar_wait(smem_u32(sc_full + j % Cfg::NSS), (j / Cfg::NSS) & 1, abort_flag, p.err);
@@ -640,6 +649,14 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
       bool warp_need = false;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
+        // the K scales come while the scores do, half a tile's at once (each read
+        // just before its use, the softmax waited for shared memory: 192 sequences
+        // of 4 heads behind 65536 int8 keys 330 -> 314 us)
+        float4 kk[KV ? 16 : 1];
+        if constexpr (KV != 0) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) kk[e] = prefix_lds16(ks_at + hf * 256 + e * 16);
+        }
         float v[64];
         tmem_ld32(sa + hf * 64, *reinterpret_cast<float(*)[32]>(v));
         tmem_ld32(sa + hf * 64 + 32, *reinterpret_cast<float(*)[32]>(v + 32));
@@ -648,7 +665,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, KV>::kThreads, PrefixCfg<D, KV>::
         if constexpr (KV != 0) {
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
-            const float4 k4 = *reinterpret_cast<const float4 *>(ks + hf * 64 + e);
+            const float4 k4 = kk[e >> 2];
             mul2p(v[e], v[e + 1], k4.x, k4.y);
             mul2p(v[e + 2], v[e + 3], k4.z, k4.w);
           }
