@@ -381,6 +381,7 @@ cudaError_t launch_move(const EvictLaunch &L) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictLaunch &L) {
+  if (L.p.num_seqs == 0) return cudaMemsetAsync(L.p.cu_out, 0, sizeof(int32_t), L.stream);
   cudaError_t e = launch_select(L);
   return e == cudaSuccess ? launch_move(L) : e;
 }

@@ -215,12 +215,12 @@ fa_status_t prefix_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, const
   if ((st = check_table(block_table, "block_table", B, launch->max_seqlen_k, page_size))) return st;
   if ((st = check_cu(cu_seqlens_q, "cu_seqlens_q", B)) || (st = check_cu(cu_seqlens_k, "cu_seqlens_k", B))) return st;
   if ((st = check_tensor(out, "out", FA_BF16, 3))) return st;
-  if (out->shape[0] != Tq || out->shape[1] != Hq || out->shape[2] != D || !contiguous(out))
+  if (out->shape[0] != Tq || out->shape[1] != Hq || out->shape[2] != D || (numel(out) > 0 && !contiguous(out)))
     return fail(FA_ERR_INVALID_ARG, "out must be contiguous [%lld, %lld, %lld]", (long long)Tq, (long long)Hq, (long long)D);
   if ((uintptr_t)out->data & 15) return fail(FA_ERR_INVALID_ARG, "out must be 16-byte aligned");
   if (lse) {
     if ((st = check_tensor(lse, "lse", FA_F32, 2))) return st;
-    if (lse->shape[0] != Hq || lse->shape[1] != Tq || !contiguous(lse))
+    if (lse->shape[0] != Hq || lse->shape[1] != Tq || (numel(lse) > 0 && !contiguous(lse)))
       return fail(FA_ERR_INVALID_ARG, "lse must be contiguous [Hq=%lld, T_q=%lld]", (long long)Hq, (long long)Tq);
     if (overlaps(lse, out)) return fail(FA_ERR_INVALID_ARG, "lse must not alias out");
   }
@@ -411,7 +411,7 @@ fa_status_t weights_build(const fa_tensor_t *q, const fa_tensor_t *k_cache, cons
   if (!paged && k_cache->shape[0] < launch->total_k) return fail(FA_ERR_INVALID_ARG, "packed k_cache has fewer rows than total_k");
   if ((st = check_cu(cu_seqlens_q, "cu_seqlens_q", B)) || (st = check_cu(cu_seqlens_k, "cu_seqlens_k", B))) return st;
   if ((st = check_tensor(lse, "lse", FA_F32, 2))) return st;
-  if (lse->shape[0] != Hq || lse->shape[1] != Tq || !contiguous(lse))
+  if (lse->shape[0] != Hq || lse->shape[1] != Tq || (numel(lse) > 0 && !contiguous(lse)))
     return fail(FA_ERR_INVALID_ARG, "lse must be contiguous [Hq=%lld, T_q=%lld]", (long long)Hq, (long long)Tq);
   if ((st = check_rows3(out, "out", B, Hkv, true))) return st;
   const int64_t extent = out->shape[2];
@@ -573,14 +573,15 @@ fa_status_t evict_build(const fa_tensor_t *weights, fa_tensor_t *weights_out, co
     for (const fa_tensor_t *r : read)
       if (overlaps(moved[i], r)) return fail(FA_ERR_INVALID_ARG, "the cache must not overlap the tables or lengths");
   }
-  P.kind = 0;
-  if (B == 0) return FA_OK;
+  fa::EvictParams &p = P.ev.p;
+  memset(&P.ev, 0, sizeof P.ev);
+  P.kind = 5;
+  p.cu_out = (int32_t *)cu_seqlens_k_out->data;
+  if (B == 0) return FA_OK;   // its one entry is 0 all the same
   if (!kept->data) return fail(FA_ERR_INVALID_ARG, "kept data is NULL");
   if (launch->max_seqlen_k > 0 && (!k_cache->data || !v_cache->data || !block_table->data))
     return fail(FA_ERR_INVALID_ARG, "a required data pointer is NULL");
 
-  fa::EvictParams &p = P.ev.p;
-  memset(&P.ev, 0, sizeof P.ev);
   const int esz = dtype_size(k_cache->dtype);
   p.w = (const float *)weights->data;
   p.w_stride_b = weights->stride[0];
@@ -591,7 +592,6 @@ fa_status_t evict_build(const fa_tensor_t *weights, fa_tensor_t *weights_out, co
   p.wo_stride_h = wo->stride[1];
   p.extent_out = wo->shape[2];
   p.cu_k = (const int32_t *)cu_seqlens_k->data;
-  p.cu_out = (int32_t *)cu_seqlens_k_out->data;
   p.bt = (const int32_t *)block_table->data;
   p.bt_stride = block_table->stride[0];
   p.max_pages = block_table->shape[1];
@@ -631,7 +631,6 @@ fa_status_t evict_build(const fa_tensor_t *weights, fa_tensor_t *weights_out, co
   const int64_t keys = std::min(p.max_keys, p.extent_in), rows = B * Hkv;
   const auto fits = [&](int64_t ctas) { return rows * ctas <= 2 * sm_count() && keys <= ctas * fa::kEvictSegKeys; };
   P.ev.ctas = keys > 32768 && fits(8) ? 8 : keys > 8192 && fits(4) ? 4 : 1;
-  P.kind = 5;
   return FA_OK;
 }
 

@@ -541,8 +541,8 @@ FA_API fa_status_t fa_key_weights_plan_create(const fa_tensor_t *q, const fa_ten
  *  launch            num_seqs, max_seqlen_k; no workspace.  A sequence longer
  *                    than max_seqlen_k, L or its table records
  *                    FA_ERR_DEVICE_BOUNDS and counts as that long.
- * In place, sequences may share pages only within their first `sink` keys
- * (those never move).  A page id outside the pool is skipped and records
+ * In place, a page may stand in several block_table rows (or twice in one) only
+ * within the first `sink` keys (those never move); in block_table_out once.  A page id outside the pool is skipped and records
  * FA_ERR_DEVICE_BOUNDS.
  */
 FA_API fa_status_t fa_cache_evict(const fa_tensor_t *weights, fa_tensor_t *weights_out, const fa_tensor_t *k_cache,

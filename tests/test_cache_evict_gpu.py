@@ -212,3 +212,13 @@ def test_bad_pages_and_lengths_are_flagged():
 def test_long_rows_of_one_block_each(lens, budget, w_apart):
     """More rows than clusters are made for, and a row longer than eight blocks hold."""
     run(lens, budget, sink=5, recent=40, hkv=4, dk=64, dv=64, page=256, seed=len(lens), w_apart=w_apart)
+
+
+def test_no_sequences_and_no_keys():
+    import flashattention_forward_gb300 as fa
+    z = torch.zeros((2, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+    for n in (0, 3):
+        kept, cu = fa.cache_evict(torch.ones((n, 2, 5), device=DEV), z, z.clone(), torch.zeros(n + 1, dtype=torch.int32, device=DEV),
+                                  block_table=torch.full((n, 1), -1, dtype=torch.int32, device=DEV), page_size=16, budget=4,
+                                  max_seqlen_k=0, cu_seqlens_k_out=torch.full((n + 1,), 9, dtype=torch.int32, device=DEV))
+        assert cu.tolist() == [0] * (n + 1) and kept.cpu().tolist() == [[[-1] * 4] * 2] * n

@@ -241,3 +241,18 @@ def test_query_rows_outside_q_are_flagged_and_add_nothing(form):
     assert fa.device_error() == fa.FA_ERR_DEVICE_BOUNDS
     sl.within(out[0], ref[0][0], ref[1][0])
     assert bool((out[1] == 0).all())
+
+
+def test_no_queries_and_no_keys():
+    """Without query rows the old weights decay; without sequences or entries nothing happens."""
+    import flashattention_forward_gb300 as fa
+    k = torch.zeros((1, 16, 2, 64), dtype=torch.bfloat16, device=DEV)
+    q, lse = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((4, 0), device=DEV)
+    for n, L in ((2, 40), (2, 0), (0, 40)):
+        w = torch.rand((n, 2, L), device=DEV)
+        old = w.clone()
+        cu_k = torch.arange(0, 3 * (n + 1), 3, dtype=torch.int32, device=DEV) if L else torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+        fa.key_weights(q, k, lse, torch.zeros(n + 1, dtype=torch.int32, device=DEV), cu_k, max_seqlen_q=0,
+                       max_seqlen_k=min(L, 3), block_table=torch.zeros((n, 1), dtype=torch.int32, device=DEV), page_size=16,
+                       weights=w, beta=0.5)
+        assert torch.equal(w, 0.5 * old)
