@@ -402,8 +402,9 @@ FA_API fa_status_t fa_fwd_varlen_noalloc(const fa_tensor_t *q, const fa_tensor_t
  * prefix, and a group of one sequence or a prefix of 0 keys is fine.
  *
  * max_len and num_splits only size the work: max_len bounds lens[] (a longer
- * prefix is still attended in full), num_splits >= 1 cuts each prefix into
- * that many key ranges (fa_shared_prefix_default_splits).  launch->num_splits
+ * prefix is still attended in full), num_splits >= 1 cuts a prefix of max_len
+ * keys into that many key ranges, and shorter ones into fewer of the same
+ * length (fa_shared_prefix_default_splits).  launch->num_splits
  * >= 1 cuts the keys behind the prefix likewise, sized by max_seqlen_k -
  * max_len (fa_shared_prefix_default_own_splits).
  */
@@ -427,7 +428,8 @@ typedef struct {
  * Three kernels: the prefix pass, the sequences' own keys, the merge.
  * FA_ERR_UNSUPPORTED for packed K/V, the 5-D pages, other head dims or more
  * query rows; other errors as fa_fwd_varlen.  A page id outside the pool
- * counts as a page of zeros and records FA_ERR_DEVICE_BOUNDS.
+ * counts as a page of zeros and records FA_ERR_DEVICE_BOUNDS.  A sequence whose
+ * query rows (cu_seqlens_q) lie outside q records it too and has no result.
  */
 FA_API fa_status_t fa_fwd_shared_prefix(const fa_tensor_t *q, const fa_tensor_t *k_cache, const fa_tensor_t *v_cache,
                                  const fa_tensor_t *block_table, const fa_tensor_t *cu_seqlens_q,
@@ -487,7 +489,8 @@ FA_API int32_t fa_shared_prefix_default_own_splits(int32_t num_seqs, int32_t max
  *               for packed K); no workspace.  max_seqlen_k and max_seqlen_q
  *               bound the lengths: a longer sequence records
  *               FA_ERR_DEVICE_BOUNDS and its excess is left out.  A page id
- *               outside the pool counts as keys of zeros and records it too.
+ *               outside the pool counts as keys of zeros and records it too,
+ *               and a sequence whose query rows lie outside q adds nothing.
  * One kernel: for max_seqlen_q * Hq/Hkv <= 16 bound by reading K, otherwise
  * tensor-core tiles.  Sums are fp32 in a fixed order (the same bits each run).
  */
